@@ -1,0 +1,200 @@
+// The norms between two blocks in one pass over the rows:
+//   n = o / sqrt(mean(o^2) + eps) * w_post        norm after the block
+//   r = x + s * g * n                             gate, residual scale and sum
+//   y = r / sqrt(mean(r^2) + eps) * w_pre         norm before the next block
+// with y rounded to the activation type or to 8-bit rows with a scale.
+//
+// Bound by memory: o, x (and a full gate) read once, r and y written once, 10 bytes
+// per bf16 element.  A row belongs to one block and stays in its registers through
+// the two or three reductions it needs (sum of o^2, sum of r^2, max |y|), which is
+// what keeps it to one pass; r passes to the second norm in fp32, unrounded.
+#pragma once
+
+#include "device.cuh"
+#include "quant.cuh"
+
+namespace gdn {
+namespace bnorm {
+
+struct Args {
+    const void* o;
+    const void* x;
+    const void* gate;
+    const float* w_post;
+    const float* w_pre;
+    void* r;
+    void* y;
+    float* y_scale;
+    int D;
+    int gate_kind;       // gdn_gate
+    int gate_sigmoid;
+    float eps, res_scale;
+};
+
+// 16-byte loads that do not displace the weights from L1 (each row is read once).
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
+// Eight consecutive values of a row, kept as loaded.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 u;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = ld_stream(p); }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+template <>
+struct Raw8<float> {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = ld_stream(p);
+        b = ld_stream(p + 4);
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+    }
+};
+
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+
+// Sum over the block; every thread gets it, added in the same order.  `slot` is a
+// shared array of WARPS words that no reduction in flight uses.
+template <int WARPS>
+__device__ __forceinline__ float block_sum(float v, float* slot) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+    if constexpr (WARPS > 1) {
+        if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = slot[0];
+#pragma unroll
+        for (int i = 1; i < WARPS; ++i) v += slot[i];
+    }
+    return v;
+}
+
+// One row per block of WARPS warps, NV vectors of 8 elements per thread.
+template <typename TA, typename TR, bool kI8, int WARPS, int NV>
+__global__ void __launch_bounds__(WARPS * 32) block_norm_kernel(const __grid_constant__ Args p) {
+    constexpr int NT = WARPS * 32;
+    __shared__ float slot_o[WARPS], slot_r[WARPS];
+    __shared__ uint32_t slot_y[WARPS];
+    const int64_t row = blockIdx.x, base = row * p.D;
+    const int nv = p.D / 8;
+    const TA* o = static_cast<const TA*>(p.o);
+    const TR* x = static_cast<const TR*>(p.x);
+    const TA* gate = static_cast<const TA*>(p.gate);
+
+    Raw8<TR> xv[NV];
+    Raw8<TA> ov[NV], gv[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int v = threadIdx.x + j * NT;
+        if (v >= nv) continue;
+        if (o) ov[j].load(o + base + 8 * v);
+        xv[j].load(x + base + 8 * v);
+        if (p.gate_kind == GDN_GATE_FULL) gv[j].load(gate + base + 8 * v);
+    }
+
+    float f[NV][8];   // o, then r
+    float inv_o = 1.0f;
+    if (o) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            if (threadIdx.x + j * NT >= nv) continue;
+            ov[j].get(f[j]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum = fmaf(f[j][i], f[j][i], sum);
+        }
+        if (p.w_post) inv_o = rsqrtf(block_sum<WARPS>(sum, slot_o) / (float)p.D + p.eps);
+    }
+    float row_factor = p.res_scale * inv_o;
+    if (p.gate_kind == GDN_GATE_TOKEN) {
+        const float g = to_f32(gate[row]);
+        row_factor *= p.gate_sigmoid ? 1.0f / (1.0f + __expf(-g)) : g;
+    }
+
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int v = threadIdx.x + j * NT;
+        if (v >= nv) continue;
+        float xr[8];
+        xv[j].get(xr);
+        if (o) {
+            float g[8], w[8];
+            if (p.gate_kind == GDN_GATE_FULL) gv[j].get(g);
+            else if (p.gate_kind == GDN_GATE_CHANNEL) load8(static_cast<const float*>(p.gate) + 8 * v, g);
+            if (p.w_post) load8(p.w_post + 8 * v, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float n = f[j][i] * row_factor;
+                if (p.w_post) n *= w[i];
+                if (p.gate_kind >= GDN_GATE_CHANNEL) n *= p.gate_sigmoid ? 1.0f / (1.0f + __expf(-g[i])) : g[i];
+                f[j][i] = xr[i] + n;
+            }
+            store8(static_cast<TR*>(p.r) + base + 8 * v, f[j]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[j][i] = xr[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = fmaf(f[j][i], f[j][i], sum);
+    }
+    if (!p.y) return;
+    const float inv_r = rsqrtf(block_sum<WARPS>(sum, slot_r) / (float)p.D + p.eps);
+
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int v = threadIdx.x + j * NT;
+        if (v >= nv) continue;
+        float w[8];
+        load8(p.w_pre + 8 * v, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[j][i] = f[j][i] * inv_r * w[i];
+        if constexpr (kI8) m = quant::max_bits8(f[j], m);
+        else store8(static_cast<TA*>(p.y) + base + 8 * v, f[j]);
+    }
+    if constexpr (kI8) {
+        const quant::RowScale s = quant::row_scale(quant::block_max<WARPS>(m, slot_y));
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int v = threadIdx.x + j * NT;
+            if (v < nv) *reinterpret_cast<uint2*>(static_cast<int8_t*>(p.y) + base + 8 * v) = quant::pack_i8(f[j], s);
+        }
+        if (threadIdx.x == 0) p.y_scale[row] = s.scale;
+    }
+}
+
+}  // namespace bnorm
+}  // namespace gdn

@@ -20,9 +20,9 @@ namespace gdn {
 __device__ unsigned int g_device_error;
 
 // Bits of the error word: a tensor-core commit or a copy that never arrived, a
-// malformed cu_seqlens found by the prefill's chunk-table kernel, and a conv
-// output outside the fp16 range of the prefill workspace.
-enum : unsigned int { kErrMmaTimeout = 1u, kErrCopyTimeout = 2u, kErrSeqlens = 4u, kErrRange = 8u };
+// malformed cu_seqlens found by the prefill's chunk-table kernel, a conv output
+// outside the fp16 range of the prefill workspace, and a parent outside its group.
+enum : unsigned int { kErrMmaTimeout = 1u, kErrCopyTimeout = 2u, kErrSeqlens = 4u, kErrRange = 8u, kErrIndex = 16u };
 
 // A wait that has not completed after this long is treated as lost.
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;   // 2 s
@@ -492,28 +492,51 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8])
 }
 
 // ---------------------------------------------------------------------------
+// Programmatic dependent launch: a kernel launched with that attribute may start
+// once every block of the kernel before it has called grid_dependency_trigger (or
+// ended); what that kernel wrote is visible after grid_dependency_wait.  Without
+// the attribute both do nothing.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void grid_dependency_trigger() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void grid_dependency_wait() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// ---------------------------------------------------------------------------
 // Host side of the error word (of the module that includes this header).
 // ---------------------------------------------------------------------------
 // The status an error word stands for, most serious first: a wait that ran
-// out, then a malformed cu_seqlens, then a conv output beyond fp16.
+// out, then a malformed cu_seqlens, then a conv output beyond fp16, then an index
+// out of range.
 inline gdn_status status_of_error_word(unsigned int w) {
     if (w & (kErrMmaTimeout | kErrCopyTimeout)) return GDN_ERR_DEVICE_TIMEOUT;
     if (w & kErrSeqlens) return GDN_ERR_SEQLENS;
     if (w & kErrRange) return GDN_ERR_RANGE;
+    if (w & kErrIndex) return GDN_ERR_INDEX;
     return GDN_OK;
+}
+
+// Reads and clears the including module's error word (every module has its own:
+// hence static, so that each keeps its own copy of the function too).
+static inline cudaError_t take_error_word(unsigned int* word) {
+    *word = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(word, g_device_error, sizeof *word);
+    if (e == cudaSuccess && *word) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_device_error, &zero, sizeof zero);
+    }
+    return e;
 }
 
 // Waits for `stream`, then reads and clears the error word: the status it
 // stands for, or GDN_ERR_CUDA if a CUDA call failed (that call's error in
 // *cuda_err when given).
-inline gdn_status take_device_error(cudaStream_t stream, cudaError_t* cuda_err = nullptr) {
+static inline gdn_status take_device_error(cudaStream_t stream, cudaError_t* cuda_err = nullptr) {
     cudaError_t e = cudaStreamSynchronize(stream);
     unsigned int v = 0;
-    if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&v, g_device_error, sizeof v);
-    if (e == cudaSuccess && v) {
-        const unsigned int zero = 0;
-        e = cudaMemcpyToSymbol(g_device_error, &zero, sizeof zero);
-    }
+    if (e == cudaSuccess) e = take_error_word(&v);
     if (cuda_err) *cuda_err = e;
     return e != cudaSuccess ? GDN_ERR_CUDA : status_of_error_word(v);
 }

@@ -1,5 +1,6 @@
 // C ABI of the Gated DeltaNet mixer (include/gdn.h): argument checks and
-// kernel launches.  One translation unit holds every kernel.
+// kernel launches.  This translation unit holds the mixer's kernels and the bf16
+// projections; serve.cu holds the operators around them.
 #include "gdn.h"
 
 #include <cudaTypedefs.h>
@@ -17,6 +18,7 @@
 #include "device.cuh"
 #include "fixup.cuh"
 #include "gemm.cuh"
+#include "host.cuh"
 #include "intra.cuh"
 #include "norm.cuh"
 #include "scan.cuh"
@@ -24,38 +26,9 @@
 namespace {
 
 using gdn::ConvArgs;
+using namespace gdn::host;
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
-bool dim_ok(int d) { return d == 32 || d == 64 || d == 128; }
-
-// The CUDA error behind this thread's most recent GDN_ERR_CUDA (gdn_last_cuda_error).
-thread_local cudaError_t t_last_cuda_error = cudaSuccess;
-
-// GDN_OK for cudaSuccess; otherwise remembers e for this thread and returns GDN_ERR_CUDA.
-gdn_status cuda_status(cudaError_t e) {
-    if (e == cudaSuccess) return GDN_OK;
-    t_last_cuda_error = e;
-    return GDN_ERR_CUDA;
-}
-
-gdn_status check_config(const gdn_config* c) {
-    if (!c) return GDN_ERR_INVALID_ARG;
-    if (c->n_k_heads <= 0 || c->n_v_heads <= 0 || c->d_k <= 0 || c->d_v <= 0) return GDN_ERR_INVALID_ARG;
-    if (!(c->l2_eps >= 0.f) || !(c->norm_eps >= 0.f) || !std::isfinite(c->l2_eps) ||
-        !std::isfinite(c->norm_eps))
-        return GDN_ERR_INVALID_ARG;
-    if (c->act_dtype != GDN_BF16 && c->act_dtype != GDN_F32) return GDN_ERR_INVALID_ARG;
-    if (c->out_dtype != GDN_BF16 && c->out_dtype != GDN_F32) return GDN_ERR_INVALID_ARG;
-    if (c->state_dtype != GDN_BF16 && c->state_dtype != GDN_F32) return GDN_ERR_INVALID_ARG;
-    if (c->n_v_heads % c->n_k_heads != 0) return GDN_ERR_UNSUPPORTED;
-    if (!dim_ok(c->d_k) || !dim_ok(c->d_v)) return GDN_ERR_UNSUPPORTED;
-    if (c->conv_kernel != 4 || c->chunk != gdn::intra::C) return GDN_ERR_UNSUPPORTED;
-    if (c->prefill_segments < GDN_PREFILL_SPLIT || c->prefill_segments > GDN_PREFILL_MAX_SEGMENTS)
-        return GDN_ERR_INVALID_ARG;
-    return GDN_OK;
-}
+static_assert(kChunkTokens == gdn::intra::C, "chunk length");
 
 gdn_status check_weights(const gdn_weights* w) {
     if (!w || !w->conv_weight || !w->A_log || !w->dt_bias || !w->norm_weight) return GDN_ERR_INVALID_ARG;
@@ -250,44 +223,6 @@ cudaError_t ensure_smem(K kernel, int variant, size_t bytes) {
     return e;
 }
 
-// cuCtxGetCurrent, fetched once from the driver through the runtime.
-PFN_cuCtxGetCurrent_v4000 ctx_getter() {
-    static PFN_cuCtxGetCurrent_v4000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuCtxGetCurrent", &f, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(f);
-    });
-    return fn;
-}
-
-// cuTensorMapEncodeTiled, fetched once from the driver through the runtime.  It
-// is a driver call and needs a current context, which a host thread that has
-// made no runtime call yet does not have: the current device's primary context
-// is made current first in that case.
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    });
-    CUcontext ctx = nullptr;
-    auto get_ctx = ctx_getter();
-    if (!get_ctx || get_ctx(&ctx) != CUDA_SUCCESS) return nullptr;
-    if (!ctx) {
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess) return nullptr;
-    }
-    return fn;
-}
-
 // 3-D map over a row-major [T][H][d] tensor: boxes of 64 (d) x 1 (head) x 64
 // (tokens), 128-byte swizzle; elements past d or T read as zero.
 bool head_tile_map(CUtensorMap* m, const void* base, CUtensorMapDataType dt, int elem_bytes, int d, int H,
@@ -393,18 +328,6 @@ cudaEvent_t* thread_events(EventUse use, size_t n) {
         v.push_back(e);
     }
     return v.data();
-}
-
-// Streaming multiprocessors of the current device (cached per device).
-int sm_count() {
-    static int count[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-    if (dev < 64 && count[dev]) return count[dev];
-    int n = 0;
-    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
-    if (dev < 64) count[dev] = n;
-    return n;
 }
 
 // 2-D map over a row-major [rows][K] bf16 matrix for the projections: boxes of
@@ -1527,10 +1450,12 @@ gdn_status gdn_prefill_host(const gdn_config* cfg, const gdn_weights* w, const v
 }
 
 gdn_status gdn_check_device_error(void* stream) {
-    cudaError_t e = cudaSuccess;
-    const gdn_status s = gdn::take_device_error(static_cast<cudaStream_t>(stream), &e);
-    if (e != cudaSuccess) cuda_status(e);
-    return s;
+    cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
+    unsigned int here = 0, serve = 0;   // the error words of the library's two modules
+    if (e == cudaSuccess) e = gdn::take_error_word(&here);
+    if (e == cudaSuccess) e = gdn::take_serve_error_word(&serve);
+    if (e != cudaSuccess) return cuda_status(e);
+    return gdn::status_of_error_word(here | serve);
 }
 
 const char* gdn_last_cuda_error(void) {
@@ -1551,6 +1476,7 @@ const char* gdn_status_string(gdn_status s) {
         case GDN_ERR_WORKSPACE: return "workspace too small";
         case GDN_ERR_SEQLENS: return "cu_seqlens malformed (device check)";
         case GDN_ERR_RANGE: return "conv output beyond the fp16 range of the workspace (device check)";
+        case GDN_ERR_INDEX: return "index out of range (device check)";
     }
     return "unknown status";
 }

@@ -346,11 +346,28 @@ __device__ __forceinline__ void commit_pair_w(uint32_t bar) {
 }
 #undef GDN_ELECT2
 
-template <int BN>
+// What the pair kernel needs to know of its operand type: how many elements fill a
+// 128-byte row of a k-block, the MMA over 32 bytes of K, and the epilogue.
+struct Bf16Op {
+    using Args = gemm::Args;
+    static constexpr int BK = gemm::BK;
+    static constexpr bool kAfterQuantize = false;
+    static __host__ __device__ constexpr uint32_t idesc(int M, int N) { return idesc_bf16(M, N); }
+    static __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+        mma_pair_w(d, a, b, id, acc);
+    }
+    template <int BN>
+    static __device__ __forceinline__ void store(uint32_t taddr, const Args& p, int64_t m, int n0) {
+        store_row<BN>(taddr, p, m, n0);
+    }
+};
+
+template <int BN, class Op = Bf16Op>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-                   const __grid_constant__ Args p) {
+                   const __grid_constant__ typename Op::Args p) {
     using S = Shape2<BN>;
+    constexpr int BK = Op::BK;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t sb = (raw + 1023u) & ~1023u;
@@ -391,6 +408,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     cluster_sync();    // barriers of both CTAs initialised, tensor memory allocated
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
+    // x and its scales may still be on their way from the kernel before this one
+    if constexpr (Op::kAfterQuantize) grid_dependency_wait();
     const int kb_n = (p.K + BK - 1) / BK;
     const int64_t m_pairs = (p.M + 2 * BM - 1) / (2 * BM);
     const int64_t tiles = m_pairs * p.n_blocks;
@@ -434,7 +453,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     } else if (warp == 1) {
         // ---- MMA issuer: CTA 0 only ----
         if (rank == 0) {
-            constexpr uint32_t ID = idesc_bf16(2 * BM, BN);
+            constexpr uint32_t ID = Op::idesc(2 * BM, BN);
             const uint32_t peer = 1;
             uint32_t it = 0, ti = 0;
             bool ok = true;
@@ -455,9 +474,9 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
                     tc_fence_after();
                     const uint32_t a_src = sb + (uint32_t)s * S::STAGE;
 #pragma unroll
-                    for (int k = 0; k < BK / 16; ++k)
-                        mma_pair_w(d, sdesc(a_src + k * 32, 16, 1024), sdesc(a_src + S::A_BYTES + k * 32, 16, 1024),
-                                   ID, (kb | k) != 0);
+                    for (int k = 0; k < 4; ++k)   // 32 bytes of K each
+                        Op::mma_pair(d, sdesc(a_src + k * 32, 16, 1024), sdesc(a_src + S::A_BYTES + k * 32, 16, 1024),
+                                     ID, (kb | k) != 0);
                     commit_pair_w(empty(s));
                     commit_pair_w(map_to_rank(empty(s), peer));
                 }
@@ -486,8 +505,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
             }
             tc_fence_after();
             const int mb = (int)(t % m_pairs), nb = (int)(t / m_pairs);
-            store_row<BN>(tmem + ((uint32_t)(q * 32) << 16) + a * BN, p,
-                          (int64_t)mb * 2 * BM + (int64_t)rank * BM + row, nb * BN);
+            Op::template store<BN>(tmem + ((uint32_t)(q * 32) << 16) + a * BN, p,
+                                   (int64_t)mb * 2 * BM + (int64_t)rank * BM + row, nb * BN);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_cluster(map_to_rank(acc_empty(a), 0));

@@ -1,0 +1,339 @@
+// Dense projections in 8-bit integers on the 5th-generation tensor cores:
+//   y[m][n] = x_scale[m] * w_scale[n] * sum_k x[m][k] w[n][k]
+// kind::i8 multiplies int8 pairs and adds them in int32, so the sum is exact
+// whatever its order; it meets the scales in fp32 in the epilogue.
+//
+// Two forms:
+//   - M > 128 (prefill): the CTA-pair kernel of gemm.cuh with 128 bytes of K per
+//     k-block = 128 int8, i.e. twice the K of the bf16 form for the same operand
+//     bytes and MMA time.  Bound by the tensor cores.
+//   - M <= 128 (decode): linear_i8_rows_kernel below, bound by reading the weights.
+#pragma once
+
+#include "gemm.cuh"
+
+namespace gdn {
+namespace gemm {
+
+// D format s32, A and B int8 (signed), both K-major.
+__host__ __device__ constexpr uint32_t idesc_i8(int M, int N) {
+    return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+constexpr int BK8 = 128;   // 128 int8 = one 128-byte swizzle row along K
+
+struct I8Args : Args {
+    const float* x_scale;
+    const float* w_scale;
+    int out_f32;           // destinations are fp32 (else bf16)
+};
+
+#define GDN_ELECT "{\n\t.reg .pred e;\n\t.reg .b32 ex;\n\telect.sync ex|e, 0xffffffff;\n\t"
+__device__ __forceinline__ void mma_i8_w(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                         uint32_t accumulate) {
+    asm volatile(GDN_ELECT ".reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+                 "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_i8_pair_w(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                              uint32_t accumulate) {
+    asm volatile(GDN_ELECT ".reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "@e tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+                 "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+#undef GDN_ELECT
+
+// The output segment that holds column n.
+__device__ __forceinline__ const Seg& segment_of(const Args& p, int n) {
+    int j = 0;
+    while (j + 1 < p.n_segs && n >= p.seg[j + 1].n0) ++j;
+    return p.seg[j];
+}
+
+struct I8Op {
+    using Args = I8Args;
+    static constexpr int BK = BK8;
+    static constexpr bool kAfterQuantize = true;
+    static __host__ __device__ constexpr uint32_t idesc(int M, int N) { return idesc_i8(M, N); }
+    static __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+        mma_i8_pair_w(d, a, b, id, acc);
+    }
+    // Eight columns of row m, scaled: a segment is a multiple of 8 wide.
+    static __device__ __forceinline__ void store8(const uint32_t* r, const Args& p, int64_t m, int n8, float xs) {
+        if (n8 >= p.N || m >= p.M) return;
+        const float4 w0 = __ldg(reinterpret_cast<const float4*>(p.w_scale + n8));
+        const float4 w1 = __ldg(reinterpret_cast<const float4*>(p.w_scale + n8) + 1);
+        const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = (float)(int)r[i] * (xs * w[i]);
+        const Seg& sg = segment_of(p, n8);
+        const int64_t at = m * sg.width + (n8 - sg.n0);
+        if (p.out_f32) {
+            float4* d = reinterpret_cast<float4*>(reinterpret_cast<float*>(sg.dst) + at);
+            d[0] = make_float4(f[0], f[1], f[2], f[3]);
+            d[1] = make_float4(f[4], f[5], f[6], f[7]);
+        } else {
+            uint32_t b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) b[i] = pack_bf16(__float_as_uint(f[2 * i]), __float_as_uint(f[2 * i + 1]));
+            *reinterpret_cast<uint4*>(sg.dst + at) = make_uint4(b[0], b[1], b[2], b[3]);
+        }
+    }
+    template <int BN>
+    static __device__ __forceinline__ void store(uint32_t taddr, const Args& p, int64_t m, int n0) {
+        const float xs = m < p.M ? p.x_scale[m] : 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < BN / 32; ++c) {
+            uint32_t r[32];
+            tmem_ld32(taddr + c * 32, r);
+#pragma unroll
+            for (int g = 0; g < 4; ++g) store8(r + 8 * g, p, m, n0 + c * 32 + g * 8, xs);
+        }
+    }
+};
+
+// ---------------------------------------------------------------------------
+// Few tokens: the weights' rows are the MMA's M (128 channels a tile), the tokens
+// its N (BT = 16 .. 128, rows past M read as zeros), so a tile's time is that of
+// its 16 KiB of weights per k-block and the tokens cost little.  One persistent
+// CTA per SM with the roles of linear_kernel: TMA producer, MMA issuer, 4 epilogue
+// warps over two TMEM accumulators; the ring holds about 200 KiB in flight, several
+// times what an SM needs to draw its share of HBM.
+// When there are fewer tiles than SMs, a cluster of S CTAs shares a tile: each
+// takes a range of K, leaves its int32 sums in its shared memory, and adds up the
+// tokens that fall to it over the cluster (exact, so the split changes no bit).
+// Launched behind the kernel that makes the 8-bit rows: the weights, which that
+// kernel does not write, are fetched while it still runs.
+// ---------------------------------------------------------------------------
+template <int BT>
+struct RowsShape {
+    static_assert(BT % 16 == 0 && BT >= 16 && BT <= 128, "tokens a tile");
+    static constexpr int W_BYTES = 128 * BK8;
+    static constexpr int X_BYTES = BT * BK8;
+    static constexpr int STAGE = W_BYTES + X_BYTES;
+    static constexpr int STAGES = (200 * 1024) / STAGE;
+    static constexpr int OFF_BAR = STAGES * STAGE;
+    static constexpr int N_BARS = 2 * STAGES + 5;   // full, empty, acc_full[2], acc_empty[2], drain
+    static constexpr int SMEM = OFF_BAR + N_BARS * 8 + 8 + 1024;
+    static constexpr uint32_t TMEM_COLS = 2 * BT < 32 ? 32 : 2 * BT;
+    static_assert(STAGE % 1024 == 0, "stage alignment");
+    static_assert(SMEM <= 227 * 1024, "shared memory");
+    static_assert(STAGES * STAGE >= BT * 128 * 4, "partial sums fit where the stages were");
+};
+
+// y[m][n] of one channel n, which dst / width place.
+__device__ __forceinline__ void store1(const I8Args& p, const Seg& sg, int64_t m, int n, int acc, float ws) {
+    const float y = (float)acc * (__ldg(p.x_scale + m) * ws);
+    const int64_t at = m * sg.width + (n - sg.n0);
+    if (p.out_f32) reinterpret_cast<float*>(sg.dst)[at] = y;
+    else sg.dst[at] = __float2bfloat16_rn(y);
+}
+
+__device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+template <int BT>
+__global__ void __launch_bounds__(NT, 1)
+linear_i8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
+                      const __grid_constant__ I8Args p, int splits) {
+    using S = RowsShape<BT>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    const uint32_t sb = (raw + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (sb - raw);
+    const uint32_t bar0 = sb + S::OFF_BAR;
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (S::STAGES + s); };
+    auto acc_full = [&](int a) { return bar0 + 8u * (2 * S::STAGES + a); };
+    auto acc_empty = [&](int a) { return bar0 + 8u * (2 * S::STAGES + 2 + a); };
+    const uint32_t drain = bar0 + 8u * (2 * S::STAGES + 4);
+    volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(smem + S::OFF_BAR + S::N_BARS * 8);
+    volatile uint32_t* s_abort = s_tmem + 1;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S::STAGES; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(acc_full(a), 1);
+            mbar_init(acc_empty(a), 4);
+        }
+        mbar_init(drain, 1);
+        *s_abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(smem_u32(const_cast<uint32_t*>(s_tmem)), S::TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+
+    // this CTA's k-blocks [k_lo, k_lo + kb_n) and tiles first, first + step, ...
+    const int rank = splits > 1 ? (int)cluster_rank() : 0;
+    const int kb_all = (p.K + BK8 - 1) / BK8;
+    const int k_lo = (int)((int64_t)kb_all * rank / splits);
+    const int kb_n = (int)((int64_t)kb_all * (rank + 1) / splits) - k_lo;
+    const int tiles = p.n_blocks;
+    const int first = blockIdx.x / splits, step = gridDim.x / splits;
+    const int my_tiles = first < tiles ? (tiles - first + step - 1) / step : 0;
+
+    if (warp == 0) {
+        // ---- TMA producer (one thread) ----
+        if (lane == 0) {
+            prefetch_tmap(&tm_x);
+            prefetch_tmap(&tm_w);
+            const uint32_t total = (uint32_t)my_tiles * kb_n;
+            const uint32_t pre = total < (uint32_t)S::STAGES ? total : S::STAGES;
+            auto load_w = [&](uint32_t it, int s) {
+                const int tile = first + (int)(it / kb_n) * step, kb = k_lo + (int)(it % kb_n);
+                tma_load_2d(sb + (uint32_t)s * S::STAGE, &tm_w, kb * BK8, tile * 128, full(s));
+            };
+            auto load_x = [&](uint32_t it, int s) {
+                const int kb = k_lo + (int)(it % kb_n);
+                tma_load_2d(sb + (uint32_t)s * S::STAGE + S::W_BYTES, &tm_x, kb * BK8, 0, full(s));
+            };
+            for (uint32_t it = 0; it < pre; ++it) {
+                mbar_arrive_expect_tx(full(it), S::STAGE);
+                load_w(it, it);
+            }
+            grid_dependency_wait();
+            for (uint32_t it = 0; it < pre; ++it) load_x(it, it);
+            bool ok = true;
+            uint32_t it = pre;
+            for (; it < total; ++it) {
+                const int s = (int)(it % S::STAGES);
+                if (!mbar_wait_bounded(empty(s), ((it / S::STAGES) & 1u) ^ 1u) || *s_abort) {
+                    ok = false;
+                    break;
+                }
+                mbar_arrive_expect_tx(full(s), S::STAGE);
+                load_w(it, s);
+                load_x(it, s);
+            }
+            if (!ok) {
+                record_error(kErrCopyTimeout);
+                *s_abort = 1;
+            }
+            // the last copy armed on each stage lands before the CTA may exit
+            for (uint32_t s = 0; s < (uint32_t)S::STAGES && s < it; ++s) {
+                const uint32_t last = s + (it - 1 - s) / S::STAGES * S::STAGES;
+                mbar_wait_bounded(full(s), (last / S::STAGES) & 1u);
+            }
+        }
+    } else if (warp == 1) {
+        // ---- MMA issuer (converged warp, elected lane issues) ----
+        constexpr uint32_t ID = idesc_i8(128, BT);
+        uint32_t it = 0;
+        bool ok = true;
+        for (int ti = 0; ti < my_tiles && ok; ++ti) {
+            const uint32_t a = ti & 1u;
+            if (!mbar_wait_bounded(acc_empty(a), ((ti >> 1) & 1u) ^ 1u) || *s_abort) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint32_t d = tmem + a * BT;
+            for (int kb = 0; kb < kb_n; ++kb, ++it) {
+                const int s = (int)(it % S::STAGES);
+                if (!mbar_wait_bounded(full(s), (it / S::STAGES) & 1u) || *s_abort) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t src = sb + (uint32_t)s * S::STAGE;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)   // 32 int8 of K each
+                    mma_i8_w(d, sdesc(src + k * 32, 16, 1024), sdesc(src + S::W_BYTES + k * 32, 16, 1024), ID,
+                             (kb | k) != 0);
+                mma_commit_w(empty(s));
+            }
+            if (!ok) break;
+            mma_commit_w(acc_full(a));
+        }
+        if (!ok) {
+            record_error(kErrMmaTimeout);
+            *s_abort = 1;
+        }
+        // every MMA issued here completes before TMEM and shared memory are released
+        mma_commit_w(drain);
+        mbar_wait_bounded(drain, 0);
+    } else {
+        // ---- epilogue: this thread's channel, all tokens ----
+        const int q = warp & 3;
+        const int row = q * 32 + lane;
+        grid_dependency_wait();   // (the rows' scales)
+        bool ok = true;
+        for (int ti = 0; ti < my_tiles; ++ti) {
+            const uint32_t a = ti & 1u;
+            if (!mbar_wait_bounded(acc_full(a), (ti >> 1) & 1u) || *s_abort) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const int n = (first + ti * step) * 128 + row;
+            const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + a * BT;
+            const float ws = n < p.N ? p.w_scale[n] : 0.0f;
+            const Seg& sg = segment_of(p, n);
+#pragma unroll 1
+            for (int c = 0; c < BT / 16; ++c) {
+                uint32_t r[16];
+                tmem_ld16(taddr + c * 16, r);
+                if (splits > 1) {   // [token][channel] int32 over the stages, all read by now
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(sb + ((c * 16 + i) * 128 + row) * 4), "r"(r[i])
+                                     : "memory");
+                } else if (n < p.N) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (c * 16 + i < p.M) store1(p, sg, c * 16 + i, n, (int)r[i], ws);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive(acc_empty(a));
+        }
+        if (!ok && lane == 0) {
+            record_error(kErrMmaTimeout);
+            *s_abort = 1;
+        }
+    }
+
+    if (splits > 1) {
+        // one tile per cluster: token m of it is added up by CTA m % splits
+        cluster_sync();
+        if (warp >= 2 && !*s_abort && my_tiles > 0) {
+            const int row = (warp & 3) * 32 + lane, n = first * 128 + row;
+            if (n < p.N) {
+                const Seg& sg = segment_of(p, n);
+                const float ws = p.w_scale[n];
+                for (int m = rank; m < p.M; m += splits) {
+                    int acc = 0;
+                    for (int r = 0; r < splits; ++r) acc += ld_cluster_s32(map_to_rank(sb + (m * 128 + row) * 4, r));
+                    store1(p, sg, m, n, acc, ws);
+                }
+            }
+        }
+        cluster_sync();   // no CTA leaves while its sums may still be read
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, S::TMEM_COLS);
+    }
+}
+
+}  // namespace gemm
+}  // namespace gdn

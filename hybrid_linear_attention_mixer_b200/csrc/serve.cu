@@ -1,0 +1,551 @@
+// C ABI of the operators around the mixer in a serving step (include/gdn.h): the
+// norms between blocks, 8-bit projections, beam selection and state reordering.
+// Argument checks and launches; the kernels are in the headers named below.
+#include "gdn.h"
+
+#include <algorithm>
+#include <cstring>
+
+#include "beam.cuh"
+#include "block_norm.cuh"
+#include "device.cuh"
+#include "gemm_i8.cuh"
+#include "host.cuh"
+#include "quant.cuh"
+#include "reorder.cuh"
+
+namespace {
+
+using namespace gdn::host;
+
+// Lifts a kernel's shared-memory limit, once per device.
+template <auto Kernel>
+cudaError_t allow_smem(size_t bytes) {
+    static bool done[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && done[dev]) return cudaSuccess;
+    e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && dev < 64) done[dev] = true;
+    return e;
+}
+
+struct Span {
+    uintptr_t lo, hi;
+};
+Span span(const void* p, int64_t bytes) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+    return {a, a + (p ? (uintptr_t)bytes : 0)};
+}
+bool overlap(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
+
+bool float_dtype(int32_t d) { return d == GDN_BF16 || d == GDN_F32; }
+int elem(int32_t d) { return d == GDN_F32 ? 4 : d == GDN_BF16 ? 2 : 1; }
+
+// A launch that may start while the kernel before it on the stream still runs.
+struct Launch {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    Launch(unsigned grid, unsigned block, size_t smem, cudaStream_t st) {
+        cfg.gridDim = dim3(grid, 1, 1);
+        cfg.blockDim = dim3(block, 1, 1);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        cfg.attrs = attr;
+    }
+    Launch& overlapped(bool on) {
+        if (on) {
+            attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+        }
+        return *this;
+    }
+    Launch& cluster(unsigned n) {
+        if (n > 1) {
+            attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+            attr[cfg.numAttrs].val.clusterDim.x = n;
+            attr[cfg.numAttrs].val.clusterDim.y = 1;
+            attr[cfg.numAttrs++].val.clusterDim.z = 1;
+        }
+        return *this;
+    }
+};
+
+// ---------------------------------------------------------------------------
+// Block norms
+// ---------------------------------------------------------------------------
+template <typename TA, typename TR, bool kI8, int WARPS, int NV>
+cudaError_t launch_norm(const gdn::bnorm::Args& a, int64_t T, cudaStream_t st) {
+    gdn::bnorm::block_norm_kernel<TA, TR, kI8, WARPS, NV><<<(unsigned)T, WARPS * 32, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename TA, typename TR, bool kI8>
+cudaError_t norm_by_size(const gdn::bnorm::Args& a, int64_t T, cudaStream_t st) {
+    const int nv = a.D / 8;
+    if (nv <= 128) return launch_norm<TA, TR, kI8, 4, 1>(a, T, st);
+    if (nv <= 256) return launch_norm<TA, TR, kI8, 4, 2>(a, T, st);
+    if (nv <= 384) return launch_norm<TA, TR, kI8, 4, 3>(a, T, st);
+    if (nv <= 512) return launch_norm<TA, TR, kI8, 4, 4>(a, T, st);
+    if (nv <= 1024) return launch_norm<TA, TR, kI8, 16, 2>(a, T, st);
+    return launch_norm<TA, TR, kI8, 16, 4>(a, T, st);
+}
+
+template <typename TA, typename TR>
+cudaError_t norm_by_output(const gdn::bnorm::Args& a, int64_t T, cudaStream_t st) {
+    return a.y_scale ? norm_by_size<TA, TR, true>(a, T, st) : norm_by_size<TA, TR, false>(a, T, st);
+}
+
+// ---------------------------------------------------------------------------
+// 8-bit rows
+// ---------------------------------------------------------------------------
+template <typename T>
+cudaError_t launch_quantize(const void* x, int64_t rows, int32_t cols, int8_t* q, float* scale, cudaStream_t st) {
+    using namespace gdn::quant;
+    const T* xt = static_cast<const T*>(x);
+    const unsigned grid = (unsigned)rows;
+    const int nv = cols / 8;
+    if (nv <= 128) quantize_rows_kernel<T, 4, 1><<<grid, 128, 0, st>>>(xt, cols, q, scale);
+    else if (nv <= 384) quantize_rows_kernel<T, 4, 3><<<grid, 128, 0, st>>>(xt, cols, q, scale);
+    else if (nv <= 1024) quantize_rows_kernel<T, 8, 4><<<grid, 256, 0, st>>>(xt, cols, q, scale);
+    else quantize_rows_kernel<T, 16, 0><<<grid, 512, 0, st>>>(xt, cols, q, scale);
+    return cudaGetLastError();
+}
+
+gdn_status run_quantize(const void* x, int32_t x_dtype, int64_t rows, int32_t cols, int8_t* q, float* scale,
+                        cudaStream_t st) {
+    return cuda_status(x_dtype == GDN_BF16 ? launch_quantize<__nv_bfloat16>(x, rows, cols, q, scale, st)
+                                           : launch_quantize<float>(x, rows, cols, q, scale, st));
+}
+
+// ---------------------------------------------------------------------------
+// 8-bit projections
+// ---------------------------------------------------------------------------
+// 2-D map over a row-major [rows][K] int8 matrix: boxes of 128 (K) x box_rows,
+// 128-byte swizzle; elements past K or rows read as zero.
+bool i8_map(CUtensorMap* m, const void* base, int64_t rows, int K, int box_rows) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)K, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)K};
+    cuuint32_t box[2] = {(cuuint32_t)gdn::gemm::BK8, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Clusters of `size` CTAs of a kernel that the device holds at once, asked of the
+// runtime once per device and size.
+template <auto Kernel>
+int resident_clusters(int size, size_t smem) {
+    static int known[64][4];
+    int dev = 0, n = 0;
+    const int slot = size == 1 ? 0 : size == 2 ? 1 : size == 4 ? 2 : 3;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+    if (dev < 64 && known[dev][slot]) return known[dev][slot];
+    Launch l((unsigned)(sm_count() / size * size), gdn::gemm::NT, smem, nullptr);
+    l.cluster((unsigned)size);
+    if (size == 1) n = sm_count();
+    else if (cudaOccupancyMaxActiveClusters(&n, Kernel, &l.cfg) != cudaSuccess || n <= 0) {
+        (void)cudaGetLastError();
+        n = std::max(1, sm_count() / size);
+    }
+    if (dev < 64) known[dev][slot] = n;
+    return n;
+}
+
+template <int BN>
+cudaError_t launch_i8_pair(const void* x, const void* w, gdn::gemm::I8Args a, bool behind_quantize, cudaStream_t st) {
+    using S = gdn::gemm::Shape2<BN>;
+    constexpr auto kernel = gdn::gemm::linear_pair_kernel<BN, gdn::gemm::I8Op>;
+    CUtensorMap tm_x, tm_w;
+    if (!i8_map(&tm_x, x, a.M, a.K, gdn::gemm::BM) || !i8_map(&tm_w, w, a.N, a.K, BN / 2)) return cudaErrorInvalidValue;
+    a.n_blocks = (a.N + BN - 1) / BN;
+    a.tiles = (a.M + 2 * gdn::gemm::BM - 1) / (2 * gdn::gemm::BM) * a.n_blocks;
+    cudaError_t e = allow_smem<kernel>(S::SMEM);
+    if (e != cudaSuccess) return e;
+    const int pairs = (int)std::min<int64_t>(a.tiles, resident_clusters<kernel>(2, S::SMEM));
+    Launch l((unsigned)(2 * pairs), gdn::gemm::NT, S::SMEM, st);   // (the kernel names its cluster size)
+    l.overlapped(behind_quantize);
+    return cudaLaunchKernelEx(&l.cfg, kernel, tm_x, tm_w, a);
+}
+
+// Pair tile width for M > 128: as for bf16 (the operand bytes and the MMA time per
+// k-block are the same), over the widths that kind::i8 has at M = 256.
+int pick_bn_i8(int64_t M, int N, int pairs) {
+    static const int cand[] = {256, 224, 192, 160, 128};
+    const int64_t mp = (M + 2 * gdn::gemm::BM - 1) / (2 * gdn::gemm::BM);
+    int best = 256;
+    int64_t best_cost = -1;
+    for (int bn : cand) {
+        const int64_t tiles = mp * ((N + bn - 1) / bn);
+        const int64_t cost = (tiles + pairs - 1) / pairs * std::max<int64_t>(256 + bn, 17 * bn / 8);
+        if (best_cost < 0 || cost < best_cost) {
+            best = bn;
+            best_cost = cost;
+        }
+    }
+    return best;
+}
+
+template <int BT>
+cudaError_t launch_i8_rows(const void* x, const void* w, gdn::gemm::I8Args a, bool behind_quantize, cudaStream_t st) {
+    using S = gdn::gemm::RowsShape<BT>;
+    constexpr auto kernel = gdn::gemm::linear_i8_rows_kernel<BT>;
+    CUtensorMap tm_x, tm_w;
+    if (!i8_map(&tm_x, x, a.M, a.K, BT) || !i8_map(&tm_w, w, a.N, a.K, 128)) return cudaErrorInvalidValue;
+    a.n_blocks = (a.N + 127) / 128;
+    cudaError_t e = allow_smem<kernel>(S::SMEM);
+    if (e != cudaSuccess) return e;
+    // Split K where the tiles leave SMs idle: the k-blocks that the busiest CTA walks,
+    // and a few more for the join.
+    const int kb = (a.K + gdn::gemm::BK8 - 1) / gdn::gemm::BK8;
+    int splits = 1;
+    int64_t best = -1;
+    for (int s = 1; s <= 8 && s <= kb; s *= 2) {
+        const int at_once = resident_clusters<kernel>(s, S::SMEM);
+        if (s > 1 && a.n_blocks > at_once) break;   // one tile per cluster
+        const int64_t cost = (int64_t)((a.n_blocks + at_once - 1) / at_once) * ((kb + s - 1) / s) + (s > 1 ? 4 : 0);
+        if (best < 0 || cost < best) {
+            best = cost;
+            splits = s;
+        }
+    }
+    const int grid = splits > 1 ? a.n_blocks * splits : std::min(a.n_blocks, sm_count());
+    Launch l((unsigned)grid, gdn::gemm::NT, S::SMEM, st);
+    l.overlapped(behind_quantize).cluster((unsigned)splits);
+    return cudaLaunchKernelEx(&l.cfg, kernel, tm_x, tm_w, a, splits);
+}
+
+// 8-bit rows, then their scales, in the workspace.
+size_t i8_scale_off(int64_t M, int32_t K) { return align_up((size_t)M * (size_t)K, 256); }
+
+gdn_status run_linear_i8(const void* x, int32_t x_dtype, const float* x_scale, const int8_t* w, const float* w_scale,
+                         int64_t M, int32_t N, int32_t K, int32_t out_dtype, const gdn_out_segment* segs,
+                         int32_t n_segs, void* workspace, size_t workspace_bytes, void* stream) {
+    if (M < 0 || N <= 0 || K <= 0 || !segs || n_segs <= 0) return GDN_ERR_INVALID_ARG;
+    if ((x_dtype != GDN_I8 && !float_dtype(x_dtype)) || !float_dtype(out_dtype)) return GDN_ERR_INVALID_ARG;
+    if (n_segs > GDN_LINEAR_MAX_SEGMENTS) return GDN_ERR_UNSUPPORTED;
+    if (N % 8 != 0 || K % 16 != 0 || K > 131056) return GDN_ERR_UNSUPPORTED;
+    if (M > 0x7fffffffLL - 256) return GDN_ERR_UNSUPPORTED;   // row coordinates are int32
+    gdn::gemm::I8Args a = {};
+    a.M = M;
+    a.N = N;
+    a.K = K;
+    a.n_segs = n_segs;
+    a.out_f32 = out_dtype == GDN_F32;
+    int n0 = 0;
+    for (int i = 0; i < n_segs; ++i) {
+        const gdn_out_segment& g = segs[i];
+        if (g.width <= 0 || g.width % 8 != 0 || g.width > N - n0) return GDN_ERR_INVALID_ARG;
+        a.seg[i].dst = static_cast<__nv_bfloat16*>(g.dst);
+        a.seg[i].n0 = n0;
+        a.seg[i].width = g.width;
+        n0 += g.width;
+    }
+    if (n0 != N) return GDN_ERR_INVALID_ARG;
+    if (M == 0) return GDN_OK;
+    for (int i = 0; i < n_segs; ++i)
+        if (!segs[i].dst || !aligned(segs[i].dst, 16)) return GDN_ERR_INVALID_ARG;
+    if (!x || !w || !w_scale || !aligned(x, 16) || !aligned(w, 16) || !aligned(w_scale, 16))
+        return GDN_ERR_INVALID_ARG;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool quantize = x_dtype != GDN_I8;
+    if (quantize) {
+        if (x_scale || !workspace || !aligned(workspace, 256)) return GDN_ERR_INVALID_ARG;
+        if (workspace_bytes < gdn_linear_i8_workspace_size(M, K)) return GDN_ERR_WORKSPACE;
+        int8_t* q = static_cast<int8_t*>(workspace);
+        float* scale = reinterpret_cast<float*>(q + i8_scale_off(M, K));
+        const gdn_status s = run_quantize(x, x_dtype, M, K, q, scale, st);
+        if (s != GDN_OK) return s;
+        x = q;
+        x_scale = scale;
+    } else if (!x_scale || !aligned(x_scale, 4)) {
+        return GDN_ERR_INVALID_ARG;
+    }
+    a.x_scale = x_scale;
+    a.w_scale = w_scale;
+    cudaError_t e;
+    if (M <= 16) e = launch_i8_rows<16>(x, w, a, quantize, st);
+    else if (M <= 32) e = launch_i8_rows<32>(x, w, a, quantize, st);
+    else if (M <= 64) e = launch_i8_rows<64>(x, w, a, quantize, st);
+    else if (M <= 128) e = launch_i8_rows<128>(x, w, a, quantize, st);
+    else {
+        switch (pick_bn_i8(M, N, std::max(1, sm_count() / 2))) {
+            case 256: e = launch_i8_pair<256>(x, w, a, quantize, st); break;
+            case 224: e = launch_i8_pair<224>(x, w, a, quantize, st); break;
+            case 192: e = launch_i8_pair<192>(x, w, a, quantize, st); break;
+            case 160: e = launch_i8_pair<160>(x, w, a, quantize, st); break;
+            default: e = launch_i8_pair<128>(x, w, a, quantize, st); break;
+        }
+    }
+    return cuda_status(e);
+}
+
+// ---------------------------------------------------------------------------
+// Beam selection
+// ---------------------------------------------------------------------------
+struct BeamLayout {
+    int slices;
+    size_t cand_off, total;
+};
+
+// GDN_OK and the layout, or what is wrong with the sizes.
+gdn_status beam_layout(int32_t n_groups, int32_t n_beams, int32_t vocab, int32_t n_out, int32_t dtype, BeamLayout* L) {
+    if (n_groups < 0 || n_beams <= 0 || vocab <= 0 || n_out <= 0 || !float_dtype(dtype)) return GDN_ERR_INVALID_ARG;
+    if (n_beams > GDN_BEAM_MAX_BEAMS || n_out > GDN_BEAM_MAX_OUT || vocab > GDN_BEAM_MAX_VOCAB)
+        return GDN_ERR_UNSUPPORTED;
+    L->slices = dtype == GDN_BF16 ? gdn::beam::n_slices<__nv_bfloat16>(vocab) : gdn::beam::n_slices<float>(vocab);
+    const int64_t lists = (int64_t)n_groups * n_beams * L->slices;
+    if (lists > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;   // one block each
+    L->cand_off = align_up((size_t)lists * sizeof(gdn::beam::Stat), 256);
+    L->total = L->cand_off + align_up((size_t)lists * n_out * sizeof(uint64_t), 256);
+    return GDN_OK;
+}
+
+// ---------------------------------------------------------------------------
+// State reordering
+// ---------------------------------------------------------------------------
+// Whether two buffers of n states each share a byte.  Equal strides: where the states
+// of one fall between those of the other, modulo the stride.  Different strides: by
+// what the buffers span.
+bool buffers_collide(const gdn_state_buffer& a, const gdn_state_buffer& b, int64_t n) {
+    const Span sa = span(a.base, (n - 1) * a.stride + a.bytes), sb = span(b.base, (n - 1) * b.stride + b.bytes);
+    if (!overlap(sa, sb)) return false;
+    if (a.stride != b.stride) return true;
+    const int64_t d = (int64_t)(sb.lo - sa.lo);   // b's first state after a's (or before it)
+    const int64_t m = ((d % a.stride) + a.stride) % a.stride;
+    return m < a.bytes || m + b.bytes > a.stride;
+}
+
+template <int WMAX, int U>
+cudaError_t launch_reorder(gdn::reorder::Args a, int64_t n_groups, cudaStream_t st) {
+    const int per_item = gdn::reorder::NT * U;
+    int32_t items = 0;
+    for (int i = 0; i < a.n_buffers; ++i) {
+        a.buf[i].item0 = items;
+        items += (a.buf[i].vecs + per_item - 1) / per_item;
+    }
+    a.items = items;
+    a.total = (int64_t)items * n_groups;
+    const unsigned grid = (unsigned)std::min<int64_t>(a.total, 0x7fffffff);
+    gdn::reorder::reorder_kernel<WMAX, U><<<grid, gdn::reorder::NT, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+namespace gdn {
+cudaError_t take_serve_error_word(unsigned int* word) { return take_error_word(word); }
+}  // namespace gdn
+
+extern "C" {
+
+void gdn_norm_config_default(gdn_norm_config* cfg) {
+    if (!cfg) return;
+    cfg->dim = 2560;
+    cfg->eps = 1e-6f;
+    cfg->res_scale = 1.0f;
+    cfg->gate = GDN_GATE_NONE;
+    cfg->gate_sigmoid = 0;
+    cfg->act_dtype = GDN_BF16;
+    cfg->res_dtype = GDN_BF16;
+}
+
+gdn_status gdn_block_norm(const gdn_norm_config* cfg, const void* o, const void* x, const void* gate,
+                          const float* w_post, const float* w_pre, int64_t T, void* r, void* y, float* y_scale,
+                          void* stream) {
+    if (!cfg || cfg->dim <= 0 || !(cfg->eps >= 0.f) || !std::isfinite(cfg->eps) || !std::isfinite(cfg->res_scale))
+        return GDN_ERR_INVALID_ARG;
+    if (!float_dtype(cfg->act_dtype) || !float_dtype(cfg->res_dtype)) return GDN_ERR_INVALID_ARG;
+    if (cfg->gate < GDN_GATE_NONE || cfg->gate > GDN_GATE_FULL || T < 0) return GDN_ERR_INVALID_ARG;
+    if (cfg->dim % 8 != 0 || cfg->dim > GDN_NORM_MAX_DIM || T > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
+    if (T == 0) return GDN_OK;
+    // what goes with what
+    if (!o && (w_post || gate || r || cfg->gate != GDN_GATE_NONE)) return GDN_ERR_INVALID_ARG;
+    if (!y && (w_pre || y_scale)) return GDN_ERR_INVALID_ARG;
+    if ((cfg->gate == GDN_GATE_NONE) != !gate) return GDN_ERR_INVALID_ARG;
+    if (!x || (o && !r) || (y && !w_pre) || (!o && !y)) return GDN_ERR_INVALID_ARG;
+    const void* a16[] = {o, x, r, y, w_post, w_pre, cfg->gate == GDN_GATE_TOKEN ? nullptr : gate};
+    for (const void* p : a16)
+        if (!aligned(p, 16)) return GDN_ERR_INVALID_ARG;   // null passes
+    const int ab = elem(cfg->act_dtype), rb = elem(cfg->res_dtype);
+    if (!aligned(gate, ab) || !aligned(y_scale, 4)) return GDN_ERR_INVALID_ARG;
+    const int64_t n = T * cfg->dim;
+    const Span outs[3] = {span(r, n * rb), span(y, n * (y_scale ? 1 : ab)), span(y_scale, T * 4)};
+    const int64_t gate_bytes = cfg->gate == GDN_GATE_FULL ? n * ab : cfg->gate == GDN_GATE_TOKEN ? T * ab : cfg->dim * 4;
+    const Span ins[5] = {span(x, n * rb), span(o, n * ab), span(gate, gate_bytes), span(w_post, cfg->dim * 4),
+                         span(w_pre, cfg->dim * 4)};
+    for (int i = 0; i < 3; ++i) {
+        for (int j = i + 1; j < 3; ++j)
+            if (overlap(outs[i], outs[j])) return GDN_ERR_INVALID_ARG;
+        for (int j = 0; j < 5; ++j) {
+            const bool in_place = (i == 0 && j == 0 && r == x) || (i == 1 && j == 1 && y == o && !y_scale);
+            if (!in_place && overlap(outs[i], ins[j])) return GDN_ERR_INVALID_ARG;
+        }
+    }
+    gdn::bnorm::Args a;
+    a.o = o; a.x = x; a.gate = gate;
+    a.w_post = w_post; a.w_pre = w_pre;
+    a.r = r; a.y = y; a.y_scale = y_scale;
+    a.D = cfg->dim;
+    a.gate_kind = cfg->gate;
+    a.gate_sigmoid = cfg->gate_sigmoid;
+    a.eps = cfg->eps;
+    a.res_scale = cfg->res_scale;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool abf = cfg->act_dtype == GDN_BF16, rbf = cfg->res_dtype == GDN_BF16;
+    cudaError_t e;
+    if (abf && rbf) e = norm_by_output<__nv_bfloat16, __nv_bfloat16>(a, T, st);
+    else if (abf) e = norm_by_output<__nv_bfloat16, float>(a, T, st);
+    else if (rbf) e = norm_by_output<float, __nv_bfloat16>(a, T, st);
+    else e = norm_by_output<float, float>(a, T, st);
+    return cuda_status(e);
+}
+
+gdn_status gdn_quantize_rows(const void* x, int32_t x_dtype, int64_t rows, int32_t cols, int8_t* q, float* scale,
+                             void* stream) {
+    if (rows < 0 || cols <= 0 || !float_dtype(x_dtype)) return GDN_ERR_INVALID_ARG;
+    if (cols % 16 != 0 || rows > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;
+    if (rows == 0) return GDN_OK;
+    if (!x || !q || !scale || !aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4)) return GDN_ERR_INVALID_ARG;
+    const int64_t n = rows * cols;
+    const Span in = span(x, n * elem(x_dtype)), oq = span(q, n), os = span(scale, rows * 4);
+    if (overlap(in, oq) || overlap(in, os) || overlap(oq, os)) return GDN_ERR_INVALID_ARG;
+    return run_quantize(x, x_dtype, rows, cols, q, scale, static_cast<cudaStream_t>(stream));
+}
+
+size_t gdn_linear_i8_workspace_size(int64_t M, int32_t K) {
+    if (M < 0 || K <= 0) return 0;
+    return i8_scale_off(M, K) + align_up((size_t)M * sizeof(float), 256);
+}
+
+gdn_status gdn_linear_i8(const void* x, int32_t x_dtype, const float* x_scale, const int8_t* w, const float* w_scale,
+                         int64_t M, int32_t N, int32_t K, int32_t out_dtype, const gdn_out_segment* segs,
+                         int32_t n_segs, void* workspace, size_t workspace_bytes, void* stream) {
+    return run_linear_i8(x, x_dtype, x_scale, w, w_scale, M, N, K, out_dtype, segs, n_segs, workspace, workspace_bytes,
+                         stream);
+}
+
+gdn_status gdn_in_proj_i8(const gdn_config* cfg, const void* hidden, int32_t x_dtype, const float* x_scale,
+                          const int8_t* w_in, const float* w_scale, int64_t T, int32_t d_model, void* q, void* k,
+                          void* v, void* z, void* a, void* b, void* workspace, size_t workspace_bytes, void* stream) {
+    gdn_status s = check_config(cfg);
+    if (s != GDN_OK) return s;
+    if (T < 0 || d_model <= 0) return GDN_ERR_INVALID_ARG;
+    const int qk = cfg->n_k_heads * cfg->d_k, vz = cfg->n_v_heads * cfg->d_v, ab = cfg->n_v_heads;
+    if (ab % 8 != 0) return GDN_ERR_UNSUPPORTED;
+    const gdn_out_segment segs[6] = {{q, qk}, {k, qk}, {v, vz}, {z, vz}, {a, ab}, {b, ab}};
+    return run_linear_i8(hidden, x_dtype, x_scale, w_in, w_scale, T, 2 * qk + 2 * vz + 2 * ab, d_model, GDN_BF16, segs,
+                         6, workspace, workspace_bytes, stream);
+}
+
+gdn_status gdn_out_proj_i8(const gdn_config* cfg, const void* o, int32_t x_dtype, const float* x_scale,
+                           const int8_t* w_out, const float* w_scale, int64_t T, int32_t d_model, void* y,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+    gdn_status s = check_config(cfg);
+    if (s != GDN_OK) return s;
+    if (T < 0 || d_model <= 0) return GDN_ERR_INVALID_ARG;
+    const gdn_out_segment seg = {y, d_model};
+    return run_linear_i8(o, x_dtype, x_scale, w_out, w_scale, T, d_model, cfg->n_v_heads * cfg->d_v, GDN_BF16, &seg, 1,
+                         workspace, workspace_bytes, stream);
+}
+
+size_t gdn_beam_workspace_size(int32_t n_groups, int32_t n_beams, int32_t vocab, int32_t n_out, int32_t logits_dtype) {
+    BeamLayout L;
+    return beam_layout(n_groups, n_beams, vocab, n_out, logits_dtype, &L) == GDN_OK ? std::max<size_t>(L.total, 256) : 0;
+}
+
+gdn_status gdn_beam_select(const void* logits, int32_t logits_dtype, int64_t ld, const float* scores,
+                           const uint8_t* finished, int32_t n_groups, int32_t n_beams, int32_t vocab, int32_t n_out,
+                           int32_t pad_token, int32_t* parents, int32_t* tokens, float* out_scores, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+    BeamLayout L;
+    const gdn_status s = beam_layout(n_groups, n_beams, vocab, n_out, logits_dtype, &L);
+    if (s != GDN_OK) return s;
+    if (ld < vocab || pad_token < 0 || pad_token >= vocab) return GDN_ERR_INVALID_ARG;
+    if (n_groups == 0) return GDN_OK;
+    if (!logits || !scores || !parents || !tokens || !out_scores || !workspace) return GDN_ERR_INVALID_ARG;
+    if (!aligned(logits, elem(logits_dtype)) || !aligned(scores, 4) || !aligned(parents, 4) || !aligned(tokens, 4) ||
+        !aligned(out_scores, 4) || !aligned(workspace, 256))
+        return GDN_ERR_INVALID_ARG;
+    const int64_t rows = (int64_t)n_groups * n_beams, res = (int64_t)n_groups * n_out;
+    if (ld > (INT64_MAX / 8) / rows) return GDN_ERR_INVALID_ARG;
+    const Span outs[4] = {span(parents, res * 4), span(tokens, res * 4), span(out_scores, res * 4),
+                          span(workspace, (int64_t)L.total)};
+    const Span ins[3] = {span(logits, ((rows - 1) * ld + vocab) * elem(logits_dtype)), span(scores, rows * 4),
+                         span(finished, rows)};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = i + 1; j < 4; ++j)
+            if (overlap(outs[i], outs[j])) return GDN_ERR_INVALID_ARG;
+        for (int j = 0; j < 3; ++j) {
+            const bool in_place = i == 2 && j == 1 && out_scores == scores && n_out == n_beams;
+            if (!in_place && overlap(outs[i], ins[j])) return GDN_ERR_INVALID_ARG;
+        }
+    }
+    if (workspace_bytes < L.total) return GDN_ERR_WORKSPACE;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    gdn::beam::Args a;
+    a.logits = logits;
+    a.ld = ld;
+    a.scores = scores;
+    a.finished = finished;
+    a.W = n_beams; a.V = vocab; a.n = n_out; a.pad = pad_token; a.slices = L.slices;
+    a.stats = reinterpret_cast<gdn::beam::Stat*>(ws);
+    a.cand = reinterpret_cast<uint64_t*>(ws + L.cand_off);
+    a.parents = parents;
+    a.tokens = tokens;
+    a.out_scores = out_scores;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const unsigned grid = (unsigned)(rows * L.slices);
+    if (logits_dtype == GDN_BF16) gdn::beam::slice_kernel<__nv_bfloat16><<<grid, gdn::beam::NT, 0, st>>>(a);
+    else gdn::beam::slice_kernel<float><<<grid, gdn::beam::NT, 0, st>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_status(e);
+    constexpr size_t most = ((size_t)GDN_BEAM_MAX_BEAMS * gdn::beam::n_slices<float>(GDN_BEAM_MAX_VOCAB) +
+                             (size_t)GDN_BEAM_MAX_OUT * GDN_BEAM_MAX_OUT) * sizeof(gdn::beam::Cand);
+    static_assert(most <= 200 * 1024, "shared memory of the merge");
+    e = allow_smem<gdn::beam::merge_kernel>(most);
+    if (e != cudaSuccess) return cuda_status(e);
+    Launch l((unsigned)n_groups, gdn::beam::MT, gdn::beam::merge_smem(n_beams, L.slices, n_out), st);
+    l.overlapped(true);
+    return cuda_status(cudaLaunchKernelEx(&l.cfg, gdn::beam::merge_kernel, a));
+}
+
+gdn_status gdn_reorder_states(const int32_t* parents, int32_t n_groups, int32_t n_beams,
+                              const gdn_state_buffer* buffers, int32_t n_buffers, void* stream) {
+    if (n_groups < 0 || n_beams <= 0 || n_buffers < 0) return GDN_ERR_INVALID_ARG;
+    if (n_beams > GDN_REORDER_MAX_BEAMS || n_buffers > GDN_REORDER_MAX_BUFFERS) return GDN_ERR_UNSUPPORTED;
+    if (n_groups == 0 || n_buffers == 0) return GDN_OK;
+    if (!parents || !buffers || !aligned(parents, 4)) return GDN_ERR_INVALID_ARG;
+    const int64_t n = (int64_t)n_groups * n_beams;
+    gdn::reorder::Args a = {};
+    a.parents = parents;
+    a.W = n_beams;
+    a.n_buffers = n_buffers;
+    const Span par = span(parents, n * 4);
+    for (int i = 0; i < n_buffers; ++i) {
+        const gdn_state_buffer& b = buffers[i];
+        if (!b.base || !aligned(b.base, 16) || b.bytes <= 0 || b.bytes % 16 != 0 || b.stride % 16 != 0 ||
+            b.stride < b.bytes || b.stride > INT64_MAX / n)
+            return GDN_ERR_INVALID_ARG;
+        if (b.bytes > ((int64_t)16 << 30)) return GDN_ERR_UNSUPPORTED;   // 16-byte units are int32
+        if (overlap(par, span(b.base, (n - 1) * b.stride + b.bytes))) return GDN_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (buffers_collide(buffers[j], b, n)) return GDN_ERR_INVALID_ARG;
+        a.buf[i].base = static_cast<uint4*>(b.base);
+        a.buf[i].stride = b.stride / 16;
+        a.buf[i].vecs = (int32_t)(b.bytes / 16);
+    }
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (n_beams <= 4) e = launch_reorder<4, 4>(a, n_groups, st);
+    else if (n_beams <= 8) e = launch_reorder<8, 2>(a, n_groups, st);
+    else if (n_beams <= 16) e = launch_reorder<16, 1>(a, n_groups, st);
+    else e = launch_reorder<32, 1>(a, n_groups, st);
+    return cuda_status(e);
+}
+
+}  // extern "C"

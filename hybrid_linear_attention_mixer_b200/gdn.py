@@ -12,6 +12,9 @@ Tensors (all contiguous, on one CUDA device):
   rec_state   [N, H_v, d_v, d_k] float32         updated in place
   cu_seqlens  [N + 1] int32                      (prefill only)
   weights     dict: conv_w [C, 4], A_log [H_v], dt_bias [H_v], norm_w [d_v], float32
+The operators around the mixer (block_norm, quantize_rows, linear_i8, in_proj_i8,
+out_proj_i8, beam_select, reorder_states) name their tensors where they are defined;
+they take tensors of any one CUDA device, the current one or not.
 """
 from __future__ import annotations
 
@@ -25,6 +28,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libgdn_b200.so")
 
 _DT = {torch.bfloat16: 0, torch.float32: 1}
+_I8 = 2   # GDN_I8
 
 
 CUDA_ERROR = 3   # GDN_ERR_CUDA
@@ -52,6 +56,16 @@ class _CSegment(ctypes.Structure):
     _fields_ = [("dst", ctypes.c_void_p), ("width", ctypes.c_int32)]
 
 
+class _CNormConfig(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int32), ("eps", ctypes.c_float), ("res_scale", ctypes.c_float),
+                ("gate", ctypes.c_int32), ("gate_sigmoid", ctypes.c_int32), ("act_dtype", ctypes.c_int32),
+                ("res_dtype", ctypes.c_int32)]
+
+
+class _CStateBuffer(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("bytes", ctypes.c_int64), ("stride", ctypes.c_int64)]
+
+
 class _CWeights(ctypes.Structure):
     _fields_ = [("conv_weight", ctypes.c_void_p), ("A_log", ctypes.c_void_p),
                 ("dt_bias", ctypes.c_void_p), ("norm_weight", ctypes.c_void_p)]
@@ -61,10 +75,15 @@ _lib = None
 EXPORTS = ("gdn_config_default", "gdn_prefill_workspace_size", "gdn_prefill_segments", "gdn_prefill", "gdn_decode",
            "gdn_decode_multi", "gdn_linear", "gdn_in_proj", "gdn_out_proj", "gdn_cp_workspace_size",
            "gdn_cp_local", "gdn_cp_finish", "gdn_prefill_host_workspace_size", "gdn_prefill_host",
-           "gdn_check_device_error", "gdn_status_string", "gdn_last_cuda_error")
+           "gdn_norm_config_default", "gdn_block_norm", "gdn_quantize_rows", "gdn_linear_i8_workspace_size",
+           "gdn_linear_i8", "gdn_in_proj_i8", "gdn_out_proj_i8", "gdn_beam_workspace_size", "gdn_beam_select",
+           "gdn_reorder_states", "gdn_check_device_error", "gdn_status_string", "gdn_last_cuda_error")
 DECODE_MULTI_MAX_TOKENS = 16   # GDN_DECODE_MULTI_MAX_TOKENS
 PREFILL_SPLIT = -1             # GDN_PREFILL_SPLIT: Config.prefill_segments value that splits the chain
 LINEAR_MAX_SEGMENTS = 8        # GDN_LINEAR_MAX_SEGMENTS
+NORM_MAX_DIM = 16384           # GDN_NORM_MAX_DIM
+BEAM_MAX_BEAMS, BEAM_MAX_OUT, BEAM_MAX_VOCAB = 32, 64, 1 << 20   # GDN_BEAM_MAX_*
+REORDER_MAX_BUFFERS, REORDER_MAX_BEAMS = 128, 32                 # GDN_REORDER_MAX_*
 
 
 def lib() -> ctypes.CDLL:
@@ -104,6 +123,26 @@ def lib() -> ctypes.CDLL:
         L.gdn_prefill_host_workspace_size.restype = sz
         L.gdn_prefill_host.argtypes = [vp, vp] + [vp] * 8 + [vp, i32, i64, vp, vp, sz, vp]
         L.gdn_prefill_host.restype = ctypes.c_int
+        L.gdn_norm_config_default.argtypes = [vp]
+        L.gdn_norm_config_default.restype = None
+        L.gdn_block_norm.argtypes = [vp] * 6 + [i64] + [vp] * 4
+        L.gdn_block_norm.restype = ctypes.c_int
+        L.gdn_quantize_rows.argtypes = [vp, i32, i64, i32, vp, vp, vp]
+        L.gdn_quantize_rows.restype = ctypes.c_int
+        L.gdn_linear_i8_workspace_size.argtypes = [i64, i32]
+        L.gdn_linear_i8_workspace_size.restype = sz
+        L.gdn_linear_i8.argtypes = [vp, i32, vp, vp, vp, i64, i32, i32, i32, vp, i32, vp, sz, vp]
+        L.gdn_linear_i8.restype = ctypes.c_int
+        L.gdn_in_proj_i8.argtypes = [vp, vp, i32, vp, vp, vp, i64, i32] + [vp] * 6 + [vp, sz, vp]
+        L.gdn_in_proj_i8.restype = ctypes.c_int
+        L.gdn_out_proj_i8.argtypes = [vp, vp, i32, vp, vp, vp, i64, i32, vp, vp, sz, vp]
+        L.gdn_out_proj_i8.restype = ctypes.c_int
+        L.gdn_beam_workspace_size.argtypes = [i32] * 5
+        L.gdn_beam_workspace_size.restype = sz
+        L.gdn_beam_select.argtypes = [vp, i32, i64, vp, vp] + [i32] * 5 + [vp] * 4 + [sz, vp]
+        L.gdn_beam_select.restype = ctypes.c_int
+        L.gdn_reorder_states.argtypes = [vp, i32, i32, vp, i32, vp]
+        L.gdn_reorder_states.restype = ctypes.c_int
         L.gdn_check_device_error.argtypes = [vp]
         L.gdn_check_device_error.restype = ctypes.c_int
         L.gdn_status_string.argtypes = [ctypes.c_int]
@@ -383,10 +422,333 @@ def cp_finish(cfg: Config, w: dict, z, summaries, rank: int, state_in, workspace
     return out, state_out
 
 
+# ---------------------------------------------------------------------------
+# The operators around the mixer in a serving step
+# ---------------------------------------------------------------------------
+def _device_of(t, name):
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    return t.device
+
+
+def _shaped(t, name, dtype, device, *shape):
+    """A contiguous tensor of this dtype, device and shape: its address."""
+    if t.dtype != dtype:
+        raise TypeError("%s: dtype %s, expected %s" % (name, t.dtype, dtype))
+    if tuple(t.shape) != shape:
+        raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), shape))
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _call(fn, what, device, stream, *args):
+    """fn(*args, stream) on the tensors' device, which need not be the current one.  The
+    stream is the caller's, else that device's current one."""
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            return _call(fn, what, device, stream, *args)
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    s = fn(*args, stream.cuda_stream)
+    if s != 0:
+        raise GdnError(s, what)
+
+
+def _empty(shape, dtype, device, stream):
+    """Memory for the call to use on ``stream``: taken from that stream's pool, so that
+    neither its last user nor its next can still be at work on another stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+_GATES = {"none": 0, "token": 1, "channel": 2, "full": 3}
+_GATE_ACTS = {"linear": 0, "sigmoid": 1}
+
+
+@dataclass
+class NormConfig:
+    """The norms between two blocks (block_norm)."""
+    dim: int = 2560
+    eps: float = 1e-6
+    res_scale: float = 1.0
+    gate: str = "none"              # "token" [T], "channel" [dim] float32, "full" [T, dim]
+    gate_act: str = "linear"        # "sigmoid": the factor is sigmoid(gate)
+    act_dtype: torch.dtype = torch.bfloat16   # of o, a token or full gate, and y
+    res_dtype: torch.dtype = torch.bfloat16   # of x and r
+
+    def c(self) -> _CNormConfig:
+        return _CNormConfig(self.dim, self.eps, self.res_scale, _GATES[self.gate], _GATE_ACTS[self.gate_act],
+                            _DT[self.act_dtype], _DT[self.res_dtype])
+
+
+def block_norm(cfg: NormConfig, o, x, gate=None, w_post=None, w_pre=None, r=None, y=None, y_scale=None,
+               quantize=False, stream=None):
+    """The norm after a block, its gate, the residual sum and the norm before the next
+    block, in one pass (gdn_block_norm):
+
+        r = x + res_scale * act(gate) * rmsnorm(o) * w_post,   y = rmsnorm(r) * w_pre
+
+    o [T, dim] (None: no block, y is the norm of x), x [T, dim] the residual stream,
+    w_post / w_pre [dim] float32 (None: no norm after / no y).  ``r`` may be x and ``y``
+    may be o.  With ``quantize``, or where ``y_scale`` [T] is given, y is int8 rows.
+    Returns (r, y, y_scale), None for what there is not."""
+    dev = _device_of(x, "x")
+    T, D = x.shape[0], cfg.dim
+    act, res = cfg.act_dtype, cfg.res_dtype
+    px = _shaped(x, "x", res, dev, T, D)
+    po = pg = pp = pw = pr = py = ps = None
+    if o is not None:
+        po = _shaped(o, "o", act, dev, T, D)
+        if r is None:
+            r = _empty((T, D), res, dev, stream)
+        pr = _shaped(r, "r", res, dev, T, D)
+    elif r is not None:
+        raise ValueError("r without a block output o")
+    if gate is not None:
+        if cfg.gate == "channel":
+            pg = _shaped(gate, "gate", torch.float32, dev, D)
+        elif cfg.gate == "token":
+            pg = _shaped(gate, "gate", act, dev, T)
+        else:
+            pg = _shaped(gate, "gate", act, dev, T, D)
+    if w_post is not None:
+        pp = _shaped(w_post, "w_post", torch.float32, dev, D)
+    if w_pre is not None:
+        pw = _shaped(w_pre, "w_pre", torch.float32, dev, D)
+        if y_scale is not None or quantize:
+            if y_scale is None:
+                y_scale = _empty(T, torch.float32, dev, stream)
+            ps = _shaped(y_scale, "y_scale", torch.float32, dev, T)
+        y_dtype = torch.int8 if ps is not None else act
+        if y is None:
+            y = _empty((T, D), y_dtype, dev, stream)
+        py = _shaped(y, "y", y_dtype, dev, T, D)
+    elif y is not None or y_scale is not None or quantize:
+        raise ValueError("y without w_pre")
+    _call(lib().gdn_block_norm, "gdn_block_norm", dev, stream, ctypes.byref(cfg.c()), po, px, pg, pp, pw, T, pr, py, ps)
+    return r, y, y_scale
+
+
+def quantize_rows(x, q=None, scale=None, stream=None):
+    """Rows in 8-bit integers: x [rows, cols] bf16 or float32 -> (q int8 [rows, cols],
+    scale float32 [rows]) with x ~ scale * q.  For activations a row is a token; for a
+    linear layer's weight it is an output channel."""
+    dev = _device_of(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x [rows, cols] expected, got %s" % (tuple(x.shape),))
+    rows, cols = x.shape
+    if x.dtype not in _DT:
+        raise TypeError("x: dtype %s, expected bfloat16 or float32" % x.dtype)
+    px = _shaped(x, "x", x.dtype, dev, rows, cols)
+    if q is None:
+        q = _empty((rows, cols), torch.int8, dev, stream)
+    if scale is None:
+        scale = _empty(rows, torch.float32, dev, stream)
+    _call(lib().gdn_quantize_rows, "gdn_quantize_rows", dev, stream, px, _DT[x.dtype], rows, cols,
+          _shaped(q, "q", torch.int8, dev, rows, cols), _shaped(scale, "scale", torch.float32, dev, rows))
+    return q, scale
+
+
+def linear_i8_workspace_size(M: int, K: int) -> int:
+    return int(lib().gdn_linear_i8_workspace_size(int(M), int(K)))
+
+
+def _i8_operand(x, x_scale, name, dev, M, K, workspace, stream):
+    """(x address, dtype code, scale address, workspace address and bytes, workspace) of the
+    left operand: int8 rows with their scales, or rows that the call makes int8 itself."""
+    if x.dtype == torch.int8:
+        if x_scale is None:
+            raise ValueError("%s in int8 needs its scales" % name)
+        return (_shaped(x, name, torch.int8, dev, M, K), _I8,
+                _shaped(x_scale, name + "_scale", torch.float32, dev, M), None, 0, None)
+    if x_scale is not None:
+        raise ValueError("%s_scale is for int8 rows; %s is %s" % (name, name, x.dtype))
+    if x.dtype not in _DT:
+        raise TypeError("%s: dtype %s, expected bfloat16, float32 or int8" % (name, x.dtype))
+    px = _shaped(x, name, x.dtype, dev, M, K)
+    if workspace is None:
+        workspace = _empty(linear_i8_workspace_size(M, K), torch.uint8, dev, stream)
+    return px, _DT[x.dtype], None, _workspace(workspace, dev), workspace.numel(), workspace
+
+
+def _workspace(t, dev):
+    if t.dtype != torch.uint8 or t.device != dev or not t.is_contiguous():
+        raise ValueError("workspace must be contiguous uint8 on %s" % dev)
+    return t.data_ptr()
+
+
+def linear_i8(x, w, w_scale, x_scale=None, outs=None, out_dtype=torch.bfloat16, workspace=None, stream=None):
+    """y = (x_scale x) . (w_scale w)^T in 8-bit integers with exact int32 sums: w [N, K] int8
+    with w_scale [N] float32; x [M, K] int8 with x_scale [M], or bf16 / float32 rows that the
+    call makes int8 first (``workspace``: linear_i8_workspace_size bytes of uint8).  ``outs``
+    as in ``linear`` (bf16, or all float32); default one [M, N] tensor of ``out_dtype``.
+    Returns the list of outputs."""
+    dev = _device_of(x, "x")
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
+        raise ValueError("x [M, K] and w [N, K] expected, got %s and %s" % (tuple(x.shape), tuple(w.shape)))
+    M, K = x.shape
+    N = w.shape[0]
+    if outs is None:
+        outs = [_empty((M, N), out_dtype, dev, stream)]
+    if not 1 <= len(outs) <= LINEAR_MAX_SEGMENTS:
+        raise ValueError("1..%d output segments" % LINEAR_MAX_SEGMENTS)
+    dt = outs[0].dtype
+    if dt not in _DT:
+        raise TypeError("outs[0]: dtype %s, expected bfloat16 or float32" % dt)
+    segs = (_CSegment * len(outs))()
+    for i, o in enumerate(outs):
+        if o.dim() != 2:
+            raise ValueError("outs[%d] must be [M, width]" % i)
+        segs[i].dst = _shaped(o, "outs[%d]" % i, dt, dev, M, o.shape[1])
+        segs[i].width = o.shape[1]
+    px, xdt, pxs, ws, ws_bytes, workspace = _i8_operand(x, x_scale, "x", dev, M, K, workspace, stream)
+    _call(lib().gdn_linear_i8, "gdn_linear_i8", dev, stream, px, xdt, pxs, _shaped(w, "w", torch.int8, dev, N, K),
+          _shaped(w_scale, "w_scale", torch.float32, dev, N), M, N, K, _DT[dt], segs, len(outs), ws, ws_bytes)
+    return outs
+
+
+def in_proj_i8(cfg: Config, hidden, w_in, w_scale, hidden_scale=None, out: dict | None = None, workspace=None,
+               stream=None) -> dict:
+    """The mixer's input projection in 8-bit integers: ``in_proj`` with w_in int8 and its
+    scales [rows of w_in]; hidden as x in ``linear_i8``."""
+    dev = _device_of(hidden, "hidden")
+    T, D = hidden.shape
+    qk, vz, ab = cfg.n_k_heads * cfg.d_k, cfg.n_v_heads * cfg.d_v, cfg.n_v_heads
+    N = 2 * qk + 2 * vz + 2 * ab
+    widths = (("q", qk), ("k", qk), ("v", vz), ("z", vz), ("a", ab), ("b", ab))
+    pw, pws = _shaped(w_in, "w_in", torch.int8, dev, N, D), _shaped(w_scale, "w_scale", torch.float32, dev, N)
+    o = out if out is not None else {n: _empty((T, wd), torch.bfloat16, dev, stream) for n, wd in widths}
+    ptrs = []
+    for n, wd in widths:
+        t = o[n]
+        _check(t, n, torch.bfloat16, dev)
+        if t.numel() != T * wd:
+            raise ValueError("%s must hold [T, %d]" % (n, wd))
+        ptrs.append(t.data_ptr())
+    px, xdt, pxs, ws, ws_bytes, workspace = _i8_operand(hidden, hidden_scale, "hidden", dev, T, D, workspace, stream)
+    _call(lib().gdn_in_proj_i8, "gdn_in_proj_i8", dev, stream, ctypes.byref(cfg.c()), px, xdt, pxs, pw, pws, T, D,
+          *ptrs, ws, ws_bytes)
+    return o
+
+
+def out_proj_i8(cfg: Config, o, w_out, w_scale, o_scale=None, y=None, workspace=None, stream=None):
+    """The mixer's output projection in 8-bit integers: ``out_proj`` with w_out int8 and its
+    scales [d_model]; o as x in ``linear_i8``.  y [T, d_model] bf16."""
+    dev = _device_of(o, "o")
+    o2 = o.reshape(o.shape[0], -1) if o.is_contiguous() else o
+    T, K, D = o2.shape[0], cfg.n_v_heads * cfg.d_v, w_out.shape[0]
+    if y is None:
+        y = _empty((T, D), torch.bfloat16, dev, stream)
+    px, xdt, pxs, ws, ws_bytes, workspace = _i8_operand(o2, o_scale, "o", dev, T, K, workspace, stream)
+    _call(lib().gdn_out_proj_i8, "gdn_out_proj_i8", dev, stream, ctypes.byref(cfg.c()), px, xdt, pxs,
+          _shaped(w_out, "w_out", torch.int8, dev, D, K), _shaped(w_scale, "w_scale", torch.float32, dev, D), T, D,
+          _shaped(y, "y", torch.bfloat16, dev, T, D), ws, ws_bytes)
+    return y
+
+
+def beam_workspace_size(n_groups: int, n_beams: int, vocab: int, n_out: int, logits_dtype=torch.bfloat16) -> int:
+    return int(lib().gdn_beam_workspace_size(n_groups, n_beams, vocab, n_out, _DT[logits_dtype]))
+
+
+def beam_select(logits, scores, n_out=None, finished=None, pad_token=0, parents=None, tokens=None, out_scores=None,
+                workspace=None, stream=None):
+    """Beam search's selection over beams and vocabulary (gdn_beam_select): of all
+    scores[g, w] + log_softmax(logits[g, w])[v], the n_out (default: n_beams) best of each
+    group g, best first, ties to the lowest w * vocab + v.
+
+    logits [groups, beams, vocab] bf16 or float32 (the last dimension dense, the rows
+    evenly spaced), scores [groups, beams] float32, finished [groups, beams] uint8 or bool
+    (such a beam goes on with ``pad_token`` and its score).  Returns (parents, tokens,
+    scores), each [groups, n_out]; -1, -1, -inf where there are fewer candidates.
+    ``out_scores`` may be ``scores`` when n_out is the number of beams."""
+    dev = _device_of(logits, "logits")
+    if logits.dim() != 3:
+        raise ValueError("logits [groups, beams, vocab] expected, got %s" % (tuple(logits.shape),))
+    G, W, V = logits.shape
+    if logits.dtype not in _DT:
+        raise TypeError("logits: dtype %s, expected bfloat16 or float32" % logits.dtype)
+    dt = _DT[logits.dtype]
+    if n_out is None:
+        n_out = W
+    ld = V
+    if not logits.is_contiguous():
+        ld = logits.stride(1) if W > 1 else logits.stride(0) if G > 1 else V
+        if (V > 1 and logits.stride(2) != 1) or (G > 1 and W > 1 and logits.stride(0) != W * ld) or ld < V:
+            raise ValueError("logits: rows must be dense and evenly spaced, strides %s" % (logits.stride(),))
+    pf = None
+    if finished is not None:
+        pf = _shaped(finished, "finished", torch.bool if finished.dtype == torch.bool else torch.uint8, dev, G, W)
+    if parents is None:
+        parents = _empty((G, n_out), torch.int32, dev, stream)
+    if tokens is None:
+        tokens = _empty((G, n_out), torch.int32, dev, stream)
+    if out_scores is None:
+        out_scores = _empty((G, n_out), torch.float32, dev, stream)
+    if workspace is None:
+        workspace = _empty(beam_workspace_size(G, W, V, n_out, logits.dtype), torch.uint8, dev, stream)
+    _call(lib().gdn_beam_select, "gdn_beam_select", dev, stream, logits.data_ptr(), dt, ld,
+          _shaped(scores, "scores", torch.float32, dev, G, W), pf, G, W, V, n_out, pad_token,
+          _shaped(parents, "parents", torch.int32, dev, G, n_out), _shaped(tokens, "tokens", torch.int32, dev, G, n_out),
+          _shaped(out_scores, "out_scores", torch.float32, dev, G, n_out), _workspace(workspace, dev), workspace.numel())
+    return parents, tokens, out_scores
+
+
+class ReorderPlan:
+    """The states that ``reorder_states`` moves, checked and laid out once."""
+
+    def __init__(self, states, n_groups: int, n_beams: int):
+        if not 0 < len(states) <= REORDER_MAX_BUFFERS:
+            raise ValueError("1..%d states" % REORDER_MAX_BUFFERS)
+        self.states, self.n_groups, self.n_beams = list(states), int(n_groups), int(n_beams)
+        self.device = _device_of(states[0], "states[0]")
+        self.buffers = (_CStateBuffer * len(states))()
+        for i, t in enumerate(self.states):
+            if t.device != self.device:
+                raise ValueError("states[%d] is on %s, expected %s" % (i, t.device, self.device))
+            if t.dim() < 2 or t.shape[0] != self.n_groups * self.n_beams:
+                raise ValueError("states[%d]: shape %s, expected [%d, ...]"
+                                 % (i, tuple(t.shape), self.n_groups * self.n_beams))
+            if t.shape[0] and not t[0].is_contiguous():
+                raise ValueError("states[%d]: each sequence's state must be contiguous" % i)
+            size = t.element_size()
+            b = self.buffers[i]
+            b.base, b.bytes = t.data_ptr(), t[0].numel() * size if t.shape[0] else 0
+            # (a single sequence's stride says nothing)
+            b.stride = t.stride(0) * size if t.shape[0] > 1 else b.bytes
+
+
+def reorder_plan(states, n_groups: int, n_beams: int) -> ReorderPlan:
+    """Checks the states (tensors [n_groups * n_beams, ...], each sequence's part
+    contiguous) once, for ``reorder_states`` calls that move them again and again.  The
+    plan keeps the tensors."""
+    return ReorderPlan(states, n_groups, n_beams)
+
+
+def reorder_states(parents, states, stream=None) -> None:
+    """After a beam selection: in every state, in place, sequence g * beams + w takes what
+    sequence g * beams + parents[g, w] held (gdn_reorder_states).  parents [groups, beams]
+    int32, -1 to keep; states a list of tensors [groups * beams, ...] or a
+    ``reorder_plan`` of them."""
+    if not isinstance(states, ReorderPlan):
+        if parents.dim() != 2:
+            raise ValueError("parents [groups, beams] expected, got %s" % (tuple(parents.shape),))
+        states = ReorderPlan(states, *parents.shape)
+    dev = states.device
+    _call(lib().gdn_reorder_states, "gdn_reorder_states", dev, stream,
+          _shaped(parents, "parents", torch.int32, dev, states.n_groups, states.n_beams), states.n_groups,
+          states.n_beams, states.buffers, len(states.buffers))
+
+
 def check_device_error(stream=None) -> None:
     """Synchronise the stream and raise GdnError if the device error word holds an
-    error: a bounded wait that ran out, or a failed device check of a prefill's
-    inputs (malformed cu_seqlens, conv output beyond fp16)."""
+    error: a bounded wait that ran out, a failed device check of a prefill's
+    inputs (malformed cu_seqlens, conv output beyond fp16), or a parent outside its
+    group in reorder_states."""
     s = lib().gdn_check_device_error(_stream(stream))
     if s != 0:
         raise GdnError(s, "device")

@@ -24,8 +24,8 @@
  * recurrence above is its standard statement.
  *
  * Conventions for every call:
- *   - All tensor pointers are DEVICE pointers, contiguous, row-major, owned by
- *     the caller.  The library allocates no memory and never synchronises the
+ *   - All tensor pointers are DEVICE pointers of the current device, contiguous,
+ *     row-major, owned by the caller.  The library allocates no memory and never synchronises the
  *     stream (gdn_check_device_error excepted).
  *   - Calls are asynchronous on `stream` (a cudaStream_t passed as void*; NULL
  *     is the legacy default stream).  conv_state and rec_state are read and
@@ -40,7 +40,7 @@
  *     gdn_check_device_error reports it as GDN_ERR_DEVICE_TIMEOUT.  Checks of
  *     device-resident inputs (prefill's cu_seqlens, and the fp16 range of the
  *     conv outputs it keeps in its workspace) report through the same word
- *     (GDN_ERR_SEQLENS, GDN_ERR_RANGE).
+ *     (GDN_ERR_SEQLENS, GDN_ERR_RANGE, GDN_ERR_INDEX).
  *   - No C++ exception crosses this interface.
  *
  * Supported shapes: d_k, d_v in {32, 64, 128}; n_v_heads a multiple of
@@ -65,11 +65,13 @@ typedef enum {
     GDN_ERR_DEVICE_TIMEOUT = 4,  /* a kernel's bounded wait ran out               */
     GDN_ERR_WORKSPACE = 5,       /* workspace smaller than gdn_prefill_workspace_size */
     GDN_ERR_SEQLENS = 6,         /* (device check) cu_seqlens malformed           */
-    GDN_ERR_RANGE = 7            /* (device check) a conv output beyond the fp16 range
+    GDN_ERR_RANGE = 7,           /* (device check) a conv output beyond the fp16 range
                                     of the prefill workspace                        */
+    GDN_ERR_INDEX = 8            /* (device check) a parent outside its group       */
 } gdn_status;
 
-typedef enum { GDN_BF16 = 0, GDN_F32 = 1 } gdn_dtype;
+/* GDN_I8: rows of 8-bit integers with a scale each (gdn_linear_i8 and its kin only) */
+typedef enum { GDN_BF16 = 0, GDN_F32 = 1, GDN_I8 = 2 } gdn_dtype;
 
 typedef struct {
     int32_t n_k_heads;    /* H_k, default 16  */
@@ -316,6 +318,169 @@ gdn_status gdn_prefill_host(const gdn_config* cfg, const gdn_weights* w,
                             int32_t n_seqs, int64_t T_total, void* out,
                             void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The operators around the mixer in a serving step: the norms between two blocks,
+ * the projections in 8-bit integers, and, for beam search, the selection of the
+ * next beams and the reordering of the states that follows it.
+ * ------------------------------------------------------------------------- */
+
+/* What multiplies a block's (normed) output before it joins the residual stream. */
+typedef enum {
+    GDN_GATE_NONE = 0,
+    GDN_GATE_TOKEN = 1,     /* gate [T] act_dtype: one factor per token          */
+    GDN_GATE_CHANNEL = 2,   /* gate [dim] float32: a parameter per channel       */
+    GDN_GATE_FULL = 3       /* gate [T][dim] act_dtype                           */
+} gdn_gate;
+
+typedef struct {
+    int32_t dim;            /* row length: a multiple of 8, at most GDN_NORM_MAX_DIM; default 2560 */
+    float eps;              /* of both norms; default 1e-6 */
+    float res_scale;        /* residual scale s; default 1 */
+    int32_t gate;           /* gdn_gate; default GDN_GATE_NONE */
+    int32_t gate_sigmoid;   /* nonzero: the factor is sigmoid(gate), else gate itself */
+    int32_t act_dtype;      /* gdn_dtype of o, gate (token, full) and y; default GDN_BF16 */
+    int32_t res_dtype;      /* gdn_dtype of x and r; default GDN_BF16 */
+} gdn_norm_config;
+
+#define GDN_NORM_MAX_DIM 16384
+
+void gdn_norm_config_default(gdn_norm_config* cfg);
+
+/*
+ * The norms between two blocks in one pass: the norm after a block, its gate, the
+ * residual sum, and the norm before the next block.  For each row t:
+ *   n = o / sqrt(mean(o^2) + eps) * w_post       (w_post NULL: n = o)
+ *   r = x + s * g * n                            (g: the gate's factor; 1 without one)
+ *   y = r / sqrt(mean(r^2) + eps) * w_pre
+ * Everything is computed in fp32; r and y are each rounded once, y from the r
+ * before its rounding.
+ *   o  [T][dim] act_dtype, the block's output; NULL: no block (then w_post, gate
+ *      and r must be NULL and gate GDN_GATE_NONE): y is the norm of x
+ *   x  [T][dim] res_dtype, the residual stream;  r likewise, its new value
+ *   w_post, w_pre [dim] float32;  gate as its kind says
+ *   y  [T][dim] act_dtype, or, when y_scale is given, int8 rows and their scales
+ *      [T] float32, as gdn_quantize_rows makes them of the unrounded y;
+ *      y NULL (then w_pre and y_scale must be NULL): only the residual sum
+ * r may be x, and y (not in int8) may be o; no other two tensors may overlap.
+ * Tensors are 16-byte aligned (y_scale and a token gate: to their element).
+ * T == 0 is a no-op.  A row whose mean square is beyond fp32 (entries above about
+ * 1e19) has the norm 0; one with an infinity or a NaN gives NaN.
+ */
+gdn_status gdn_block_norm(const gdn_norm_config* cfg, const void* o, const void* x, const void* gate,
+                          const float* w_post, const float* w_pre, int64_t T, void* r, void* y,
+                          float* y_scale, void* stream);
+
+/*
+ * Rows in 8-bit integers with one scale each, symmetric about zero:
+ *   scale = max_k |x_k| / 127,  q_k = rint(127 x_k / max_k |x_k|)   (ties to even)
+ * so x_k is about scale q_k, to half a scale.  A row of zeros has the scale 0 and
+ * zeros.  A row that holds an infinity or a NaN has the scale NaN and zeros: what
+ * is computed from it is NaN.  For activations a row is a token; for a weight
+ * [N][K] it is an output channel.
+ *   x [rows][cols] GDN_BF16 or GDN_F32, 16-byte aligned; cols a multiple of 16
+ *   (else GDN_ERR_UNSUPPORTED); q [rows][cols] int8, 16-byte aligned; scale [rows]
+ * x and q may not overlap.  rows == 0 is a no-op.
+ */
+gdn_status gdn_quantize_rows(const void* x, int32_t x_dtype, int64_t rows, int32_t cols, int8_t* q,
+                             float* scale, void* stream);
+
+/*
+ * Dense projection in 8-bit integers with a scale per token and per channel:
+ *   y[m][n] = x_scale[m] * w_scale[n] * sum_k x[m][k] w[n][k]
+ * The sum is exact (int32, on the tensor cores); it is converted to fp32, multiplied
+ * by the two scales' fp32 product and rounded to out_dtype.
+ *   x  [M][K]: GDN_I8 with its scales x_scale [M]; or GDN_BF16 / GDN_F32 with
+ *      x_scale NULL: the call makes the 8-bit rows itself (gdn_quantize_rows) in
+ *      its workspace of gdn_linear_i8_workspace_size bytes, 256-byte aligned
+ *   w  [N][K] int8, w_scale [N] float32
+ *   K a multiple of 16, at most 131056 (128 * 128 * K must fit in 31 bits); N a
+ *   multiple of 8 (else GDN_ERR_UNSUPPORTED).  The columns of y are split over segs
+ *   as in gdn_linear; dst holds out_dtype (GDN_BF16 or GDN_F32).
+ * x, w and the destinations are 16-byte aligned.  The scales may be anything,
+ * NaN and infinities included.  M == 0 is a no-op.
+ */
+size_t gdn_linear_i8_workspace_size(int64_t M, int32_t K);
+gdn_status gdn_linear_i8(const void* x, int32_t x_dtype, const float* x_scale, const int8_t* w,
+                         const float* w_scale, int64_t M, int32_t N, int32_t K, int32_t out_dtype,
+                         const gdn_out_segment* segs, int32_t n_segs, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* gdn_in_proj and gdn_out_proj in 8-bit integers: hidden / o of x_dtype as in
+ * gdn_linear_i8 (workspace for d_model, or for H_v*d_v), bf16 outputs. */
+gdn_status gdn_in_proj_i8(const gdn_config* cfg, const void* hidden, int32_t x_dtype, const float* x_scale,
+                          const int8_t* w_in, const float* w_scale, int64_t T, int32_t d_model, void* q, void* k,
+                          void* v, void* z, void* a, void* b, void* workspace, size_t workspace_bytes,
+                          void* stream);
+gdn_status gdn_out_proj_i8(const gdn_config* cfg, const void* o, int32_t x_dtype, const float* x_scale,
+                           const int8_t* w_out, const float* w_scale, int64_t T, int32_t d_model, void* y,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* Limits of gdn_beam_select. */
+#define GDN_BEAM_MAX_BEAMS 32
+#define GDN_BEAM_MAX_OUT 64
+#define GDN_BEAM_MAX_VOCAB (1 << 20)
+
+/*
+ * Beam search's selection over beams and vocabulary.  For each of n_groups requests
+ * with n_beams beams, the candidates (w, v) have the score
+ *   scores[w] + logits[w][v] - log(sum_u exp(logits[w][u]))
+ * and the n_out best are returned, best first; of equal scores the lower
+ * w * vocab + v comes first.  A candidate whose score is not finite is none: a
+ * masked token (logit -inf), a beam not in use (score -inf), a beam whose logits
+ * are all -inf or hold a NaN or a +inf.  Scores are compared in fp64 before they
+ * are rounded.
+ *   logits [n_groups*n_beams] rows of vocab entries, GDN_BF16 or GDN_F32, `ld`
+ *          entries apart (ld >= vocab), aligned to an entry
+ *   scores [n_groups][n_beams] float32
+ *   finished [n_groups][n_beams] uint8, may be NULL: nonzero for a beam that has
+ *          ended; its one candidate is (w, pad_token) with its score as it is, and
+ *          its logits are not read
+ *   parents, tokens int32 and out_scores float32 [n_groups][n_out]: the beam within
+ *          the group that each result continues, its token, its score; where there
+ *          are fewer than n_out candidates the rest are -1, -1 and -inf
+ * out_scores may be scores if n_out == n_beams; no other two tensors may overlap.
+ * 1 <= n_beams <= 32, 1 <= n_out <= 64, 1 <= vocab <= 2^20 (larger:
+ * GDN_ERR_UNSUPPORTED); 0 <= pad_token < vocab; n_groups == 0 is a no-op.  workspace
+ * of gdn_beam_workspace_size bytes (0: unsupported sizes), 256-byte aligned, its
+ * contents need not be initialised.
+ */
+size_t gdn_beam_workspace_size(int32_t n_groups, int32_t n_beams, int32_t vocab, int32_t n_out,
+                               int32_t logits_dtype);
+gdn_status gdn_beam_select(const void* logits, int32_t logits_dtype, int64_t ld, const float* scores,
+                           const uint8_t* finished, int32_t n_groups, int32_t n_beams, int32_t vocab,
+                           int32_t n_out, int32_t pad_token, int32_t* parents, int32_t* tokens,
+                           float* out_scores, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Largest number of buffers one gdn_reorder_states call takes, and of beams. */
+#define GDN_REORDER_MAX_BUFFERS 128
+#define GDN_REORDER_MAX_BEAMS 32
+
+/* One buffer of per-sequence states: sequence i's `bytes` bytes start at base +
+ * i * stride.  base 16-byte aligned, bytes and stride multiples of 16, bytes > 0,
+ * stride >= bytes. */
+typedef struct {
+    void* base;
+    int64_t bytes;
+    int64_t stride;
+} gdn_state_buffer;
+
+/*
+ * Reorders states after a beam selection, in place and in one launch: in every
+ * buffer, sequence g * n_beams + w takes the state that sequence
+ * g * n_beams + parents[g][w] had before the call.  parents [n_groups][n_beams]
+ * int32; -1 keeps the sequence's own state.  Parents may repeat and permute in any
+ * way.  A parent outside [-1, n_beams) records GDN_ERR_INDEX in the device error
+ * word, and its group is then left as it was.
+ * The recurrent and conv states of gdn_prefill and gdn_decode (of any layer count)
+ * are such buffers.  Buffers may interleave but no two states may overlap (else
+ * GDN_ERR_INVALID_ARG; buffers of different strides that span the same memory are
+ * refused too), and parents may not lie in them.  n_groups == 0 or n_buffers == 0 is a no-op; more
+ * than GDN_REORDER_MAX_BUFFERS buffers or GDN_REORDER_MAX_BEAMS beams:
+ * GDN_ERR_UNSUPPORTED.  No workspace.
+ */
+gdn_status gdn_reorder_states(const int32_t* parents, int32_t n_groups, int32_t n_beams,
+                              const gdn_state_buffer* buffers, int32_t n_buffers, void* stream);
+
 /* Capacity, in bytes, of the fixed scratch array used by gdn_prefill_noalloc. */
 #define GDN_NOALLOC_SCRATCH_BYTES ((size_t)64 << 20)
 
@@ -366,7 +531,8 @@ gdn_status gdn_prefill_noalloc(const gdn_config* cfg, const gdn_weights* w,
 /* Synchronises `stream`, then reads and clears the device error word that
  * bounded waits and the prefill's device checks write.  GDN_OK, or the most
  * serious error recorded since the last call: GDN_ERR_DEVICE_TIMEOUT, then
- * GDN_ERR_SEQLENS, then GDN_ERR_RANGE; GDN_ERR_CUDA if a CUDA call failed. */
+ * GDN_ERR_SEQLENS, then GDN_ERR_RANGE, then GDN_ERR_INDEX; GDN_ERR_CUDA if a CUDA
+ * call failed. */
 gdn_status gdn_check_device_error(void* stream);
 
 /* Static string for a status code. */
