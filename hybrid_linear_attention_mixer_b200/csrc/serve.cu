@@ -287,6 +287,8 @@ gdn_status run_linear_i8(const void* x, int32_t x_dtype, const float* x_scale, c
 // ---------------------------------------------------------------------------
 // Beam selection
 // ---------------------------------------------------------------------------
+constexpr int kBeamVecs = 8;   // 16-byte vectors per thread of a slice
+
 struct BeamLayout {
     int slices;
     size_t cand_off, total;
@@ -297,7 +299,8 @@ gdn_status beam_layout(int32_t n_groups, int32_t n_beams, int32_t vocab, int32_t
     if (n_groups < 0 || n_beams <= 0 || vocab <= 0 || n_out <= 0 || !float_dtype(dtype)) return GDN_ERR_INVALID_ARG;
     if (n_beams > GDN_BEAM_MAX_BEAMS || n_out > GDN_BEAM_MAX_OUT || vocab > GDN_BEAM_MAX_VOCAB)
         return GDN_ERR_UNSUPPORTED;
-    L->slices = dtype == GDN_BF16 ? gdn::beam::n_slices<__nv_bfloat16>(vocab) : gdn::beam::n_slices<float>(vocab);
+    const int len = gdn::beam::slice_len(elem(dtype), kBeamVecs);
+    L->slices = (vocab + len - 1) / len;
     const int64_t lists = (int64_t)n_groups * n_beams * L->slices;
     if (lists > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;   // one block each
     L->cand_off = align_up((size_t)lists * sizeof(gdn::beam::Stat), 256);
@@ -500,11 +503,11 @@ gdn_status gdn_beam_select(const void* logits, int32_t logits_dtype, int64_t ld,
     a.out_scores = out_scores;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const unsigned grid = (unsigned)(rows * L.slices);
-    if (logits_dtype == GDN_BF16) gdn::beam::slice_kernel<__nv_bfloat16><<<grid, gdn::beam::NT, 0, st>>>(a);
-    else gdn::beam::slice_kernel<float><<<grid, gdn::beam::NT, 0, st>>>(a);
+    if (logits_dtype == GDN_BF16) gdn::beam::slice_kernel<__nv_bfloat16, kBeamVecs><<<grid, gdn::beam::NT, 0, st>>>(a);
+    else gdn::beam::slice_kernel<float, kBeamVecs><<<grid, gdn::beam::NT, 0, st>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_status(e);
-    constexpr size_t most = ((size_t)GDN_BEAM_MAX_BEAMS * gdn::beam::n_slices<float>(GDN_BEAM_MAX_VOCAB) +
+    constexpr size_t most = ((size_t)GDN_BEAM_MAX_BEAMS * (GDN_BEAM_MAX_VOCAB / gdn::beam::slice_len(4, kBeamVecs)) +
                              (size_t)GDN_BEAM_MAX_OUT * GDN_BEAM_MAX_OUT) * sizeof(gdn::beam::Cand);
     static_assert(most <= 200 * 1024, "shared memory of the merge");
     e = allow_smem<gdn::beam::merge_kernel>(most);

@@ -380,6 +380,30 @@ def test_beam_select_rows_not_finite():
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_beam_select_masks_of_the_lowest_value(dt):
+    """Masks by the type's lowest finite value: such tokens are candidates still, behind all
+    others; a row of nothing else is an even distribution."""
+    G, W, V, n = 3, 2, 17000, 12
+    logits, scores = beam_case(G, W, V, dt, 19)
+    low = torch.finfo(DT[dt]).min
+    rng = np.random.default_rng(20)
+    logits.masked_fill_(torch.from_numpy(rng.random((G, W, V)) < 0.5).to(DEV), low)
+    logits[1, :, 5:] = low          # 5 tokens left in each beam, and one tie of many
+    logits[2, 1] = low
+    scores[2, 0] = scores[2, 1] - 9
+    check_beam(logits, scores, n, gdn.beam_select(logits, scores, n_out=n))
+
+
+def test_beam_select_large_logits():
+    """Rows with a large common offset, and of either sign of a large value."""
+    G, W, V, n = 4, 2, 9000, 6
+    logits, scores = beam_case(G, W, V, "f32", 21)
+    for g, off in enumerate((1e4, -3e5, 1e20, 3e38)):
+        logits[g] += off
+    check_beam(logits, scores, n, gdn.beam_select(logits, scores, n_out=n))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("V", [300, 20000, 33001])
 def test_beam_select_ties(dt, V):
     """Equal logits go to the lowest token, equal beams to the lowest beam, at any alignment:
