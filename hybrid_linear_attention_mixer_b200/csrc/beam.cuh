@@ -3,18 +3,19 @@
 //   lowest w * V + v.
 //
 // Within one row the order of the scores is the order of the logits, so one pass
-// over the logits suffices: slice_kernel reads a slice of a row once, keeps it in
-// registers, and leaves its sum of exponentials and its n largest logits;
-// merge_kernel then joins a group's slices, adds the rows' offsets in fp64 and ranks
-// the few candidates left.  Bound by reading the logits (a small group: by the
-// latency of the two dependent launches).
+// over the logits suffices: slice_kernel reads a slice of a row once, tile by tile,
+// and leaves its sum of exponentials and its n largest logits; merge_kernel then joins
+// a group's slices, adds the rows' offsets in fp64 and ranks the few candidates left.
+// Bound by reading the logits (a small group: by the latency of the two dependent
+// launches).
 //
-// The selection in a slice: with every thread's largest logit known, any bound that
-// n thread maxima reach is reached by at least n logits; a few bisection steps find
-// one that not many more reach.  The vectors that reach it go to shared memory, where
-// their logits are ranked exactly, by 64-bit keys (logit, then lowest index).  Where
-// ties make that too many (a row of equal logits) the bound is found exactly, over
-// logits and then over indexes, from a second reading of the slice.
+// The slice is streamed without synchronisation: each thread keeps its largest logit and
+// its sum of exponentials about a reference of its own.  Then, any bound that n thread
+// maxima reach is reached by at least n logits; a few bisection steps find one that not
+// many more reach.  The threads that reach it read their vectors once more (from L2), and
+// the logits that do are ranked exactly, by 64-bit keys (logit, then lowest index).  Where
+// ties make them too many (a row of equal logits), the bound is found exactly, over logits
+// and then over indexes, by more such readings.
 #pragma once
 
 #include "device.cuh"
@@ -23,22 +24,24 @@ namespace gdn {
 namespace beam {
 
 constexpr int NT = 256;             // threads of a slice block
-constexpr int VECS = 256;           // 16-byte vectors a slice collects
+constexpr int VPT = 4;              // 16-byte vectors per thread of a tile
 constexpr int CAP = 512;            // candidates a slice ranks
 constexpr int MT = 512;             // threads of a merge block
 constexpr int kMaxBeams = GDN_BEAM_MAX_BEAMS;
 constexpr int kMaxOut = GDN_BEAM_MAX_OUT;
-static_assert(kMaxOut <= NT && NT <= CAP && kMaxOut <= MT, "candidate lists");
+static_assert(kMaxOut <= NT && kMaxOut <= MT, "candidate lists");
 
-// A slice is NT * VPT vectors of 16 bytes.  A row's slices and the elements of a thread
-// go by element number, wherever the row starts in memory: equal rows have bit-equal
-// sums, so their candidates tie.
-__host__ __device__ constexpr int slice_len(int elem_bytes, int vpt) { return NT * vpt * (16 / elem_bytes); }
+// A tile is NT * VPT vectors of 16 bytes, a slice some tiles.  A row's slices and the
+// elements of a thread go by element number, wherever the row starts in memory: equal
+// rows have bit-equal sums, so their candidates tie.
+__host__ __device__ constexpr int tile_len(int elem_bytes) { return NT * VPT * (16 / elem_bytes); }
 
-// sum of exp(x) over a slice = sum * exp(ref).  sum is NaN where the slice holds a NaN or
-// +inf, and 0 with ref = -inf where it holds nothing else than -inf.
+// The sum of exp(x) over a slice: sum * 2^c * exp(-top * kScale), or, c being NaN,
+// sum * exp(top).  sum is NaN where the slice holds a NaN or +inf; top is its largest
+// logit, -inf (then sum is 0 or NaN) where it holds nothing else.
 struct Stat {
-    double sum, ref;
+    double sum;
+    float c, top;
 };
 
 struct Args {
@@ -46,7 +49,8 @@ struct Args {
     int64_t ld;
     const float* scores;
     const uint8_t* finished;   // or null
-    int W, V, n, pad, slices;
+    int W, V, n, pad, slices, tiles;   // tiles of a slice
+    int keys_in_smem;          // the merge holds a group's candidates in shared memory
     Stat* stats;               // [rows][slices]
     uint64_t* cand;            // [rows][slices][n] keys, descending, 0 = none
     int32_t* parents;
@@ -98,10 +102,19 @@ template <>
 struct Vec<__nv_bfloat16> {
     static constexpr int N = 8;
     static constexpr uint32_t kNone = 0xff80ff80u;   // -inf
-    // (a maximum that ignores NaN, like fmaxf)
-    static __device__ __forceinline__ float top(uint4 u) {
-        const __nv_bfloat162 a = __hmax2(as2(u.x), as2(u.y)), b = __hmax2(as2(u.z), as2(u.w)), c = __hmax2(a, b);
-        return __bfloat162float(__hmax(c.x, c.y));
+    // the largest of some vectors, NaN ignored as in fmaxf
+    template <int K>
+    static __device__ __forceinline__ float top(const uint4 (&u)[K]) {
+        __nv_bfloat162 m[4] = {as2(u[0].x), as2(u[0].y), as2(u[0].z), as2(u[0].w)};
+#pragma unroll
+        for (int j = 1; j < K; ++j) {
+            m[0] = __hmax2(m[0], as2(u[j].x));
+            m[1] = __hmax2(m[1], as2(u[j].y));
+            m[2] = __hmax2(m[2], as2(u[j].z));
+            m[3] = __hmax2(m[3], as2(u[j].w));
+        }
+        const __nv_bfloat162 c = __hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3]));
+        return fmaxf(__low2float(c), __high2float(c));
     }
     static __device__ __forceinline__ __nv_bfloat162 as2(uint32_t w) { return reinterpret_cast<__nv_bfloat162&>(w); }
     static __device__ __forceinline__ float2 pair(uint4 u, int i) {
@@ -122,8 +135,14 @@ template <>
 struct Vec<float> {
     static constexpr int N = 4;
     static constexpr uint32_t kNone = 0xff800000u;
-    static __device__ __forceinline__ float top(uint4 u) {
-        return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
+    template <int K>
+    static __device__ __forceinline__ float top(const uint4 (&u)[K]) {
+        float m = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < K; ++j)
+            m = fmaxf(fmaxf(fmaxf(m, __uint_as_float(u[j].x)), fmaxf(__uint_as_float(u[j].y), __uint_as_float(u[j].z))),
+                      __uint_as_float(u[j].w));
+        return m;
     }
     static __device__ __forceinline__ float2 pair(uint4 u, int i) {
         return i == 0 ? make_float2(__uint_as_float(u.x), __uint_as_float(u.y))
@@ -194,39 +213,146 @@ __device__ __forceinline__ uint4 load_vec(const T* x, int i0, int V, int shift) 
     return u;
 }
 
-template <typename T, int VPT>
+// A bound that at least n of the NT thread maxima reach and not many more, by one warp
+// that holds NT / 32 of them per lane; found only if more than n are above -inf.
+__device__ __forceinline__ bool find_bound(const float (&mine)[NT / 32], float top, int n, float* bound) {
+    int valid = 0;
+    uint32_t least = 0xffffffffu;
+#pragma unroll
+    for (int i = 0; i < NT / 32; ++i) {
+        if (mine[i] > -INFINITY) {
+            ++valid;
+            least = min(least, ordered(mine[i]));
+        }
+    }
+    valid = __reduce_add_sync(0xffffffffu, valid);
+    least = __reduce_min_sync(0xffffffffu, least);
+    if (valid <= n) return false;
+    uint32_t lo = least, hi = ordered(top);   // at least n reach lo, fewer reach anything above hi
+    int at_lo = valid;
+    while (at_lo > n + 8 && hi > lo) {
+        const uint32_t mid = lo + (hi - lo + 1) / 2;
+        const float b = from_ordered(mid);
+        int c = 0;
+#pragma unroll
+        for (int i = 0; i < NT / 32; ++i) c += mine[i] >= b;
+        c = __reduce_add_sync(0xffffffffu, c);
+        if (c >= n) {
+            lo = mid;
+            at_lo = c;
+        } else {
+            hi = mid - 1;
+        }
+    }
+    *bound = from_ordered(lo);
+    return true;
+}
+
+// The fast sum: exp(x) / 2^c is 2^(x log2e - c) in one fused operation, c an integer near
+// the largest x so far.  log2e in fp32 is 1.3e-8 (kScale) too large, which scales x: that
+// is taken back at the slice's top, so what is left goes by the distance from it.
+// kSpan: how far above c a maximum may lie; kMaxTop: the size of x up to which c is exact.
+constexpr float kSpan = 32.0f, kMaxTop = 65536.0f;
+constexpr double kScale = (double)kLog2e * kLn2 - 1.0;
+
+// 2^k for an integer k <= 0 (0 below the normal numbers)
+__device__ __forceinline__ double pow2(float k) {
+    return k > -1000.0f ? __hiloint2double((1023 + (int)k) << 20, 0) : 0.0;
+}
+
+// A thread's largest logit and its sum of exponentials, in units of 2^c.
+struct Running {
+    float m = -INFINITY, c = -2.0f * kMaxTop;
+    double sum = 0.0;
+    template <typename T>
+    __device__ __forceinline__ void add(const uint4 (&v)[VPT]) {
+        const float tm = Vec<T>::top(v);   // (NaN show in the sum)
+        m = fmaxf(m, tm);
+        if (tm * kLog2e > c + kSpan) {
+            const float up = ceilf(fminf(tm, kMaxTop) * kLog2e);
+            sum *= pow2(c - up);
+            c = up;
+        }
+        float2 s[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+            for (int e = 0; e < Vec<T>::N / 2; ++e) {
+                const float2 y = fma2(Vec<T>::pair(v[j], e), make_float2(kLog2e, kLog2e), make_float2(-c, -c));
+                s[e & 1] = add2(s[e & 1], make_float2(exp2_fast(y.x), exp2_fast(y.y)));
+            }
+        const float2 both = add2(s[0], s[1]);
+        sum += (double)(both.x + both.y);
+    }
+};
+
+template <typename T>
 __global__ void __launch_bounds__(NT, 4) slice_kernel(const __grid_constant__ Args p) {
     using X = Vec<T>;
-    constexpr int N = X::N;
-    __shared__ float s_max[NT];
+    constexpr int N = X::N, kStep = NT * N, kTile = kStep * VPT;
+    __shared__ float s_max[NT], s_c[NT / 32];
     __shared__ double s_sum[NT / 32];
     __shared__ int s_count[NT / 32];
-    __shared__ uint4 s_vec[VECS];
-    __shared__ int s_at[VECS];
+    __shared__ int s_list[NT];       // first elements of the threads that reach the bound
     __shared__ uint64_t s_key[CAP];
-    __shared__ int s_vecs, s_n;
+    __shared__ int s_listed, s_n;
     __shared__ float s_bound;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t row = blockIdx.x / p.slices;
-    const int slice = blockIdx.x % p.slices;
+    const int64_t row = blockIdx.x / (unsigned)p.slices;
+    const int slice = blockIdx.x % (unsigned)p.slices;
     if (!row_live(p, row)) {
         grid_dependency_trigger();
         return;
     }
     const T* x = static_cast<const T*>(p.logits) + row * p.ld;
-    const int first = slice * slice_len(sizeof(T), VPT) + tid * N;   // this thread's first element
+    const int first = slice * p.tiles * kTile + tid * N;   // this thread's first element
+    const int tiles = min(p.tiles, (p.V - slice * p.tiles * kTile + kTile - 1) / kTile);
     const int shift = (int)(reinterpret_cast<uintptr_t>(x) & 15u);
-    constexpr int kStep = NT * N;
 
-    uint4 v[VPT];
+    auto load_tile = [&](uint4 (&u)[VPT], int t) {
+        if (t >= tiles) return;
+        const int i0 = first + t * kTile, tile0 = (slice * p.tiles + t) * kTile;
+        if (shift == 0 && tile0 + kTile <= p.V) {
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) v[j] = load_vec<T>(x, first + j * kStep, p.V, shift);
-    float m = X::top(v[0]);
+            for (int j = 0; j < VPT; ++j) u[j] = ld_once(x + i0 + j * kStep);
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < VPT; ++j) {
+                const uint4 a = load_vec<T>(x, i0 + j * kStep, p.V, shift);
 #pragma unroll
-    for (int j = 1; j < VPT; ++j) m = fmaxf(m, X::top(v[j]));
-    m = fmaxf(m, -INFINITY);   // (only NaN: they show in the sum)
-    s_max[tid] = m;
-    if (tid == 0) s_vecs = s_n = 0;
+                for (int k = 0; k < VPT; ++k)
+                    if (k == j) u[k] = a;
+            }
+        }
+    };
+    // one tile's vectors are on their way while the other's are worked on
+    uint4 even[VPT], odd[VPT];
+    Running run;
+    load_tile(even, 0);
+#pragma unroll 1
+    for (int t = 0; t < tiles; t += 2) {
+        load_tile(odd, t + 1);
+        run.add<T>(even);
+        if (t + 1 >= tiles) break;
+        load_tile(even, t + 2);
+        run.add<T>(odd);
+    }
+
+    s_max[tid] = run.m;
+    if (tid == 0) {
+        s_listed = s_n = 0;
+        s_bound = -3.402823466e38f;
+    }
+    float c = run.c;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, d));
+    double sum = run.sum * pow2(run.c - c);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (lane == 0) {
+        s_sum[warp] = sum;
+        s_c[warp] = c;
+    }
     __syncthreads();
     float mine[NT / 32], top = -INFINITY;
 #pragma unroll
@@ -236,120 +362,79 @@ __global__ void __launch_bounds__(NT, 4) slice_kernel(const __grid_constant__ Ar
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-
-    if (warp == 0) {   // a bound that at least n thread maxima reach and not many more
-        int valid = 0;
-        uint32_t least = 0xffffffffu;
-#pragma unroll
-        for (int i = 0; i < NT / 32; ++i) {
-            if (mine[i] > -INFINITY) {
-                ++valid;
-                least = min(least, ordered(mine[i]));
-            }
-        }
-        valid = __reduce_add_sync(0xffffffffu, valid);
-        least = __reduce_min_sync(0xffffffffu, least);
-        uint32_t lo = ordered(-3.402823466e38f);
-        if (valid > p.n) {   // at least n maxima reach lo, fewer reach anything above hi
-            const int enough = p.n + 8;
-            uint32_t hi = ordered(top);
-            int at_lo = valid;
-            lo = least;
-            while (at_lo > enough && hi > lo) {
-                const uint32_t mid = lo + (hi - lo + 1) / 2;
-                const float b = from_ordered(mid);
-                int c = 0;
-#pragma unroll
-                for (int i = 0; i < NT / 32; ++i) c += mine[i] >= b;
-                c = __reduce_add_sync(0xffffffffu, c);
-                if (c >= p.n) {
-                    lo = mid;
-                    at_lo = c;
-                } else {
-                    hi = mid - 1;
-                }
-            }
-        }
-        if (lane == 0) s_bound = from_ordered(lo);
-    }
-
-    // The slice's sum of exponentials, about a reference near its top.  exp(x - ref) is
-    // 2^(x log2e - c), c an integer, in one fused operation for tops of ordinary size:
-    // log2e in fp32 is 1.3e-8 off, which scales x; (x - top) log2e for others, whose x
-    // that would move too far.
-    double ref;
-    float2 s2[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-    if (fabsf(top) <= 64.0f) {
-        const float c = ceilf(top * kLog2e);
-        ref = (double)c * kLn2;
-#pragma unroll
-        for (int j = 0; j < VPT; ++j)
-#pragma unroll
-            for (int e = 0; e < N / 2; ++e) {
-                const float2 t = fma2(X::pair(v[j], e), make_float2(kLog2e, kLog2e), make_float2(-c, -c));
-                s2[e & 1] = add2(s2[e & 1], make_float2(exp2_fast(t.x), exp2_fast(t.y)));
-            }
-    } else {
-        ref = top;
-#pragma unroll
-        for (int j = 0; j < VPT; ++j)
-#pragma unroll
-            for (int e = 0; e < N / 2; ++e) {
-                const float2 t = X::pair(v[j], e);
-                // (-inf and nothing else: no sum, but a NaN has to show)
-                s2[0].x += top > -INFINITY || isnan(t.x) ? exp2_fast((t.x - top) * kLog2e) : 0.0f;
-                s2[0].y += top > -INFINITY || isnan(t.y) ? exp2_fast((t.y - top) * kLog2e) : 0.0f;
-            }
-    }
-    double sum = ((double)s2[0].x + (double)s2[0].y) + ((double)s2[1].x + (double)s2[1].y);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (lane == 0) s_sum[warp] = sum;
-    __syncthreads();
-
-    // the vectors that reach the bound, then their logits that do
-    float bound = s_bound;
-    if (m >= bound) {
-#pragma unroll
-        for (int j = 0; j < VPT; ++j)
-            if (X::top(v[j]) >= bound) {
-                const int k = atomicAdd(&s_vecs, 1);
-                if (k < VECS) {
-                    s_vec[k] = v[j];
-                    s_at[k] = first + j * kStep;
-                }
-            }
-    }
-    if (tid == 0) {
+    const bool redo_sum = top > -INFINITY && !(fabsf(top) <= kMaxTop);
+    const int finder = blockIdx.x % (NT / 32);   // (spreads this work over the schedulers)
+    if (warp == finder) {
+        float b;
+        if (find_bound(mine, top, p.n, &b) && lane == 0) s_bound = b;
+    } else if (warp == (finder + 1) % (NT / 32) && lane == 0 && !redo_sum) {
+        float most = s_c[0];
+        for (int i = 1; i < NT / 32; ++i) most = fmaxf(most, s_c[i]);
         double t = 0.0;
-        for (int i = 0; i < NT / 32; ++i) t += s_sum[i];
-        p.stats[row * p.slices + slice] = Stat{t, ref};
+        for (int i = 0; i < NT / 32; ++i) t += s_sum[i] * pow2(s_c[i] - most);
+        p.stats[row * p.slices + slice] = Stat{t, most, top};
     }
     __syncthreads();
-    const int vecs = s_vecs;
-    if (vecs <= VECS) {
-        for (int i = tid; i < vecs * N; i += NT) {
-            const int k = i / N, e = i % N;
-            const float f = to_f32(reinterpret_cast<const T*>(&s_vec[k])[e]);
-            if (f >= bound) {
-                const int at = atomicAdd(&s_n, 1);
-                if (at < CAP) s_key[at] = make_key(f, s_at[k] + e);
-            }
-        }
-    }
-    __syncthreads();
-    if (vecs > VECS || s_n > CAP) {
-        // Too many reach it.  The n-th largest logit itself ...
-        auto count = [&](auto&& pred) {   // logits of the slice that pred(value, index) takes
-            int c = 0;
+    float bound = s_bound;
+    auto each_vec = [&](auto&& use) {   // use(vector, index) for the thread's vectors of the slice
+#pragma unroll 1
+        for (int t = 0; t < tiles; ++t)
 #pragma unroll 1
             for (int j = 0; j < VPT; ++j) {
-                const int i0 = first + j * kStep;
-                const uint4 u = load_vec<T>(x, i0, p.V, shift);
-#pragma unroll
-                for (int e = 0; e < N; ++e) c += pred(X::get(u, e), i0 + e);
+                const int i0 = first + t * kTile + j * kStep;
+                use(load_vec<T>(x, i0, p.V, shift), i0);
             }
-            return block_count(c, s_count);
+    };
+    if (redo_sum) {   // about the top itself
+        sum = 0.0;
+        each_vec([&](uint4 u, int) {
+            float part = 0.0f;
+#pragma unroll
+            for (int e = 0; e < N; ++e) part += exp2_fast((X::get(u, e) - top) * kLog2e);
+            sum += (double)part;
+        });
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (lane == 0) s_sum[warp] = sum;
+        __syncthreads();
+        if (tid == 0) {
+            double t = 0.0;
+            for (int i = 0; i < NT / 32; ++i) t += s_sum[i];
+            p.stats[row * p.slices + slice] = Stat{t, __int_as_float(0x7fffffff), top};
+        }
+    }
+
+    // the threads that reach the bound, and of their vectors the logits that do
+    if (run.m >= bound) s_list[atomicAdd(&s_listed, 1)] = first;
+    __syncthreads();
+    const int per = tiles * VPT;
+    for (int i = tid; i < s_listed * per; i += NT) {
+        const int i0 = s_list[i / per] + i % per * kStep;   // (kTile is VPT kStep)
+        const uint4 u[1] = {load_vec<T>(x, i0, p.V, shift)};
+        if (X::top(u) >= bound) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float f = X::get(u[0], e);
+                if (f >= bound) {
+                    const int at = atomicAdd(&s_n, 1);
+                    if (at < CAP) s_key[at] = make_key(f, i0 + e);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    if (s_n > CAP) {
+        // Too many reach it.  The n-th largest logit itself ...
+        auto each = [&](auto&& use) {   // use(value, index)
+            each_vec([&](uint4 u, int i0) {
+#pragma unroll
+                for (int e = 0; e < N; ++e) use(X::get(u, e), i0 + e);
+            });
+        };
+        auto count = [&](auto&& pred) {
+            int n = 0;
+            each([&](float f, int i) { n += pred(f, i); });
+            return block_count(n, s_count);
         };
         uint32_t lo = ordered(bound), hi = ordered(top);
         while (hi > lo) {
@@ -361,7 +446,7 @@ __global__ void __launch_bounds__(NT, 4) slice_kernel(const __grid_constant__ Ar
         bound = from_ordered(lo);
         // ... and the index of the last one of its kind that is still among the n
         const int above = count([&](float f, int) { return f > bound; });
-        int i_lo = 0, i_hi = p.V - 1;
+        int i_lo = slice * p.tiles * kTile, i_hi = min(p.V, i_lo + tiles * kTile) - 1;
         while (i_lo < i_hi) {
             const int mid = i_lo + (i_hi - i_lo) / 2;
             if (above + count([&](float f, int i) { return f == bound && i <= mid; }) >= p.n) i_hi = mid;
@@ -369,16 +454,9 @@ __global__ void __launch_bounds__(NT, 4) slice_kernel(const __grid_constant__ Ar
         }
         if (tid == 0) s_n = 0;
         __syncthreads();
-#pragma unroll 1
-        for (int j = 0; j < VPT; ++j) {
-            const int i0 = first + j * kStep;
-            const uint4 u = load_vec<T>(x, i0, p.V, shift);
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const float f = X::get(u, e);
-                if (f > bound || (f == bound && i0 + e <= i_lo)) s_key[atomicAdd(&s_n, 1)] = make_key(f, i0 + e);
-            }
-        }
+        each([&](float f, int i) {
+            if (f > bound || (f == bound && i <= i_lo)) s_key[atomicAdd(&s_n, 1)] = make_key(f, i);
+        });
         __syncthreads();
     }
     grid_dependency_trigger();   // (the merge may be set up; it waits for this grid's end)
@@ -432,9 +510,16 @@ __device__ __forceinline__ void rank_all(const Cand* c, int total, F&& use) {
     }
 }
 
-// Shared memory of a merge block: list heads, then candidates.
+// Shared memory of a merge block: list heads, candidates, then the group's keys if they
+// are held there (up to kMaxKeyBytes).
+constexpr size_t kMaxKeyBytes = 64 * 1024;
+constexpr int kMaxLists = 4096;        // of a group
+constexpr size_t kMaxMergeSmem = (kMaxLists + (size_t)kMaxOut * kMaxOut) * sizeof(Cand) + kMaxKeyBytes;
+static_assert(kMaxMergeSmem <= 225 * 1024, "shared memory of the merge");
+inline size_t merge_key_bytes(int W, int slices, int n) { return (size_t)W * slices * n * sizeof(uint64_t); }
 inline size_t merge_smem(int W, int slices, int n) {
-    return ((size_t)W * slices + (size_t)n * n) * sizeof(Cand);
+    const size_t keys = merge_key_bytes(W, slices, n);
+    return ((size_t)W * slices + (size_t)n * n) * sizeof(Cand) + (keys <= kMaxKeyBytes ? keys : 0);
 }
 
 // One block per group.
@@ -453,23 +538,49 @@ __global__ void __launch_bounds__(MT) merge_kernel(const __grid_constant__ Args 
     if (tid < kMaxOut) sel[tid] = -1;
     if (tid == 0) s_n = 0;
     grid_dependency_wait();
+    const uint64_t* keys = p.cand + row0 * p.slices * p.n;
+    if (p.keys_in_smem) {   // (of rows that left none too: whatever is there is not used)
+        uint64_t* mine = reinterpret_cast<uint64_t*>(cand + p.n * p.n);
+        for (int i = tid; i < lists * p.n; i += MT) mine[i] = keys[i];
+        keys = mine;
+    }
 
     for (int w = warp; w < p.W; w += MT / 32) {
         const int64_t row = row0 + w;
         const float score = p.scores[row];
         const bool fin = p.finished && p.finished[row];
-        double off = score, top = -INFINITY;
+        double off = score;
+        float top = -INFINITY;
         if (!fin && isfinite(score)) {
             const Stat* st = p.stats + row * p.slices;
-            for (int s = lane; s < p.slices; s += 32) top = fmax(top, st[s].ref);
+            float c = -INFINITY;
+            bool fast = true;
+            for (int s = lane; s < p.slices; s += 32) {
+                top = fmaxf(top, st[s].top);
+                c = fmaxf(c, st[s].c);
+                fast &= !isnan(st[s].c);
+            }
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, d));
-            double sum = 0.0;
-            for (int s = lane; s < p.slices; s += 32)
-                sum += st[s].ref > -INFINITY ? st[s].sum * exp(st[s].ref - top) : st[s].sum;
+            for (int d = 16; d > 0; d >>= 1) {
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, d));
+            }
+            fast = __all_sync(0xffffffffu, fast);
+            double sum = 0.0;   // of exp(x) / (2^c exp(-top kScale)), or / exp(top)
+            for (int s = lane; s < p.slices; s += 32) {
+                const Stat t = st[s];
+                double f = 0.0;   // (no logits: t.sum is 0, or the NaN that has to show)
+                if (!(t.top > -INFINITY)) f = 1.0;
+                else if (fast)   // (exp of a number below 2e-3, and of 1e-6 where it matters)
+                    f = pow2(t.c - c) * (1.0 - ((double)t.top - (double)top) * kScale);
+                else f = exp((isnan(t.c) ? (double)t.top : (double)t.c * kLn2 - (double)t.top * kScale) - (double)top);
+                sum += t.sum * f;
+            }
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            // off + (logit - top) is the score
             off -= log(sum);   // (nothing but -inf: +inf; a NaN or +inf among the logits: NaN)
+            if (fast && top > -INFINITY) off += (double)top * (1.0 + kScale) - (double)c * kLn2;
         }
         if (lane == 0) {
             ref[w] = top;
@@ -484,7 +595,7 @@ __global__ void __launch_bounds__(MT) merge_kernel(const __grid_constant__ Args 
         const int w = l / p.slices;
         Cand c{0, 0, 0};
         if (kind[w] == 1) {
-            const uint64_t k = p.cand[((row0 + w) * p.slices + l % p.slices) * p.n + e];
+            const uint64_t k = keys[l * p.n + e];
             if (k) {
                 c.score = ordered64(((double)from_ordered((uint32_t)(k >> 32)) - ref[w]) + offset[w]);
                 c.at = (uint32_t)w * p.V + (0xffffffffu - (uint32_t)k);

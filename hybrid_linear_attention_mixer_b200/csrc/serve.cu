@@ -287,10 +287,10 @@ gdn_status run_linear_i8(const void* x, int32_t x_dtype, const float* x_scale, c
 // ---------------------------------------------------------------------------
 // Beam selection
 // ---------------------------------------------------------------------------
-constexpr int kBeamVecs = 8;   // 16-byte vectors per thread of a slice
+constexpr int kBeamTiles = 8, kBeamWaves = 6;
 
 struct BeamLayout {
-    int slices;
+    int slices, tiles;
     size_t cand_off, total;
 };
 
@@ -299,8 +299,14 @@ gdn_status beam_layout(int32_t n_groups, int32_t n_beams, int32_t vocab, int32_t
     if (n_groups < 0 || n_beams <= 0 || vocab <= 0 || n_out <= 0 || !float_dtype(dtype)) return GDN_ERR_INVALID_ARG;
     if (n_beams > GDN_BEAM_MAX_BEAMS || n_out > GDN_BEAM_MAX_OUT || vocab > GDN_BEAM_MAX_VOCAB)
         return GDN_ERR_UNSUPPORTED;
-    const int len = gdn::beam::slice_len(elem(dtype), kBeamVecs);
-    L->slices = (vocab + len - 1) / len;
+    // Tiles of a slice: enough slices for several waves of blocks, then longer ones, whose
+    // selection costs less per logit.
+    const int tile = gdn::beam::tile_len(elem(dtype)), row_tiles = (vocab + tile - 1) / tile;
+    const int64_t waves = (int64_t)n_groups * n_beams * row_tiles / (kBeamWaves * 4 * 148);
+    L->tiles = (int)std::min<int64_t>(std::max<int64_t>(waves, 1), kBeamTiles);
+    // (a merge block holds a list head per slice of the group)
+    while ((int64_t)n_beams * ((row_tiles + L->tiles - 1) / L->tiles) > gdn::beam::kMaxLists) ++L->tiles;
+    L->slices = (row_tiles + L->tiles - 1) / L->tiles;
     const int64_t lists = (int64_t)n_groups * n_beams * L->slices;
     if (lists > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;   // one block each
     L->cand_off = align_up((size_t)lists * sizeof(gdn::beam::Stat), 256);
@@ -495,7 +501,9 @@ gdn_status gdn_beam_select(const void* logits, int32_t logits_dtype, int64_t ld,
     a.ld = ld;
     a.scores = scores;
     a.finished = finished;
-    a.W = n_beams; a.V = vocab; a.n = n_out; a.pad = pad_token; a.slices = L.slices;
+    a.W = n_beams; a.V = vocab; a.n = n_out; a.pad = pad_token;
+    a.slices = L.slices; a.tiles = L.tiles;
+    a.keys_in_smem = gdn::beam::merge_key_bytes(n_beams, L.slices, n_out) <= gdn::beam::kMaxKeyBytes;
     a.stats = reinterpret_cast<gdn::beam::Stat*>(ws);
     a.cand = reinterpret_cast<uint64_t*>(ws + L.cand_off);
     a.parents = parents;
@@ -503,14 +511,11 @@ gdn_status gdn_beam_select(const void* logits, int32_t logits_dtype, int64_t ld,
     a.out_scores = out_scores;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const unsigned grid = (unsigned)(rows * L.slices);
-    if (logits_dtype == GDN_BF16) gdn::beam::slice_kernel<__nv_bfloat16, kBeamVecs><<<grid, gdn::beam::NT, 0, st>>>(a);
-    else gdn::beam::slice_kernel<float, kBeamVecs><<<grid, gdn::beam::NT, 0, st>>>(a);
+    if (logits_dtype == GDN_BF16) gdn::beam::slice_kernel<__nv_bfloat16><<<grid, gdn::beam::NT, 0, st>>>(a);
+    else gdn::beam::slice_kernel<float><<<grid, gdn::beam::NT, 0, st>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_status(e);
-    constexpr size_t most = ((size_t)GDN_BEAM_MAX_BEAMS * (GDN_BEAM_MAX_VOCAB / gdn::beam::slice_len(4, kBeamVecs)) +
-                             (size_t)GDN_BEAM_MAX_OUT * GDN_BEAM_MAX_OUT) * sizeof(gdn::beam::Cand);
-    static_assert(most <= 200 * 1024, "shared memory of the merge");
-    e = allow_smem<gdn::beam::merge_kernel>(most);
+    e = allow_smem<gdn::beam::merge_kernel>(gdn::beam::kMaxMergeSmem);
     if (e != cudaSuccess) return cuda_status(e);
     Launch l((unsigned)n_groups, gdn::beam::MT, gdn::beam::merge_smem(n_beams, L.slices, n_out), st);
     l.overlapped(true);

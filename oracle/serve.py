@@ -74,11 +74,11 @@ def log_softmax(x):
         return x - m - np.log(np.exp(x - m).sum(-1, keepdims=True))
 
 
-# A thread adds exponentials in fp32 in sums of 16 (15 U32), each off by 2 ulp and an
-# argument rounded once or twice (below 10 U32 where it matters); log2(e) in fp32 is 1.4e-8
-# off and scales logits of up to 64; the rest is in fp64.  25 U32 + 64 * 1.4e-8 < 2.5e-6 of
-# the sum, so of the log-sum-exp absolutely; twice that is allowed.  The published scores
-# are rounded to fp32 besides.
+# A thread adds exponentials in fp32 in sums of 16 at most (15 U32), each off by 2 ulp and
+# an argument rounded once or twice (below 10 U32 where it matters); log2(e) in fp32 is
+# 1.4e-8 off and scales a logit's distance from the top, below 64 where it matters; the
+# rest is in fp64.  25 U32 + 64 * 1.4e-8 < 2.5e-6 of the sum, so of the log-sum-exp
+# absolutely; twice that is allowed.  The published scores are rounded to fp32 besides.
 BEAM_ERR = 5e-6
 
 
