@@ -9,13 +9,14 @@
 // Bound by reading the logits (a small group: by the latency of the two dependent
 // launches).
 //
-// The slice is streamed without synchronisation: each thread keeps its largest logit and
-// its sum of exponentials about a reference of its own.  Then, any bound that n thread
-// maxima reach is reached by at least n logits; a few bisection steps find one that not
-// many more reach.  The threads that reach it read their vectors once more (from L2), and
-// the logits that do are ranked exactly, by 64-bit keys (logit, then lowest index).  Where
-// ties make them too many (a row of equal logits), the bound is found exactly, over logits
-// and then over indexes, by more such readings.
+// A warp takes a slice and streams it: each lane keeps its sum of exponentials, about a
+// reference of its own, and its largest logit of each tile.  Then, any bound that n of
+// these maxima (or of maxima over several tiles) reach is reached by at least n logits; a
+// few bisection steps find one that not many more reach.  The vectors behind the tile
+// maxima that reach it are read once more (from L2), and the logits that do are ranked
+// exactly, by 64-bit keys (logit, then lowest index).  Where ties make them too many (a row of equal logits), the
+// bound is found exactly, over logits and then over indexes, by more such readings.
+// Nothing synchronises warps, so one's selection runs beside the others' streams.
 #pragma once
 
 #include "device.cuh"
@@ -23,18 +24,22 @@
 namespace gdn {
 namespace beam {
 
-constexpr int NT = 256;             // threads of a slice block
-constexpr int VPT = 4;              // 16-byte vectors per thread of a tile
-constexpr int CAP = 512;            // candidates a slice ranks
+constexpr int WARPS = 4;            // slices (warps) of a slice block
+constexpr int VPT = 4;              // 16-byte vectors per lane of a tile
+constexpr int TILES = 32;           // most tiles of a slice
+constexpr int GROUPS = 8;           // groups of its tiles, whose maxima the bound is found from
+constexpr int SETS = GROUPS * 32;
+constexpr int LISTED = 256;         // tile maxima that a slice follows up
+constexpr int CAP = 256;            // candidates a slice ranks
 constexpr int MT = 512;             // threads of a merge block
 constexpr int kMaxBeams = GDN_BEAM_MAX_BEAMS;
 constexpr int kMaxOut = GDN_BEAM_MAX_OUT;
-static_assert(kMaxOut <= NT && kMaxOut <= MT, "candidate lists");
+static_assert(2 * kMaxOut <= SETS && 2 * kMaxOut <= CAP && kMaxOut <= MT, "candidate lists");
 
-// A tile is NT * VPT vectors of 16 bytes, a slice some tiles.  A row's slices and the
-// elements of a thread go by element number, wherever the row starts in memory: equal
-// rows have bit-equal sums, so their candidates tie.
-__host__ __device__ constexpr int tile_len(int elem_bytes) { return NT * VPT * (16 / elem_bytes); }
+// A tile is 32 * VPT vectors of 16 bytes, a slice some tiles.  A row's slices and the
+// elements of a lane go by element number, wherever the row starts in memory: equal rows
+// have bit-equal sums, so their candidates tie.
+__host__ __device__ constexpr int tile_len(int elem_bytes) { return 32 * VPT * (16 / elem_bytes); }
 
 // The sum of exp(x) over a slice: sum * 2^c * exp(-top * kScale), or, c being NaN,
 // sum * exp(top).  sum is NaN where the slice holds a NaN or +inf; top is its largest
@@ -49,7 +54,9 @@ struct Args {
     int64_t ld;
     const float* scores;
     const uint8_t* finished;   // or null
-    int W, V, n, pad, slices, tiles;   // tiles of a slice
+    int W, V, n, pad, slices;
+    int tiles;                 // of a row; slice s has [s tiles / slices, (s + 1) tiles / slices)
+    unsigned total;            // slices of all rows
     int keys_in_smem;          // the merge holds a group's candidates in shared memory
     Stat* stats;               // [rows][slices]
     uint64_t* cand;            // [rows][slices][n] keys, descending, 0 = none
@@ -181,18 +188,6 @@ __device__ __forceinline__ uint4 ld_shifted(const uint8_t* p, int shift) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Block-wide sum of small counts (every thread gets it).
-__device__ __forceinline__ int block_count(int c, int* slot) {
-    c = __reduce_add_sync(0xffffffffu, c);
-    __syncthreads();   // the slots' last readers are done
-    if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = c;
-    __syncthreads();
-    int t = 0;
-#pragma unroll
-    for (int i = 0; i < NT / 32; ++i) t += slot[i];
-    return t;
-}
-
 // A row is live when it can give candidates from its logits.
 __device__ __forceinline__ bool row_live(const Args& p, int64_t row) {
     return !(p.finished && p.finished[row]) && isfinite(p.scores[row]);
@@ -213,13 +208,13 @@ __device__ __forceinline__ uint4 load_vec(const T* x, int i0, int V, int shift) 
     return u;
 }
 
-// A bound that at least n of the NT thread maxima reach and not many more, by one warp
-// that holds NT / 32 of them per lane; found only if more than n are above -inf.
-__device__ __forceinline__ bool find_bound(const float (&mine)[NT / 32], float top, int n, float* bound) {
+// A bound that at least n of the SETS maxima reach and not many more (n + 8, but for
+// ties); each lane holds GROUPS of them.  -FLT_MAX where no more than n are above -inf.
+__device__ __forceinline__ float find_bound(const float (&mine)[GROUPS], float top, int n) {
     int valid = 0;
     uint32_t least = 0xffffffffu;
 #pragma unroll
-    for (int i = 0; i < NT / 32; ++i) {
+    for (int i = 0; i < GROUPS; ++i) {
         if (mine[i] > -INFINITY) {
             ++valid;
             least = min(least, ordered(mine[i]));
@@ -227,7 +222,7 @@ __device__ __forceinline__ bool find_bound(const float (&mine)[NT / 32], float t
     }
     valid = __reduce_add_sync(0xffffffffu, valid);
     least = __reduce_min_sync(0xffffffffu, least);
-    if (valid <= n) return false;
+    if (valid <= n) return -3.402823466e38f;
     uint32_t lo = least, hi = ordered(top);   // at least n reach lo, fewer reach anything above hi
     int at_lo = valid;
     while (at_lo > n + 8 && hi > lo) {
@@ -235,7 +230,7 @@ __device__ __forceinline__ bool find_bound(const float (&mine)[NT / 32], float t
         const float b = from_ordered(mid);
         int c = 0;
 #pragma unroll
-        for (int i = 0; i < NT / 32; ++i) c += mine[i] >= b;
+        for (int i = 0; i < GROUPS; ++i) c += mine[i] >= b;
         c = __reduce_add_sync(0xffffffffu, c);
         if (c >= n) {
             lo = mid;
@@ -244,8 +239,7 @@ __device__ __forceinline__ bool find_bound(const float (&mine)[NT / 32], float t
             hi = mid - 1;
         }
     }
-    *bound = from_ordered(lo);
-    return true;
+    return from_ordered(lo);
 }
 
 // The fast sum: exp(x) / 2^c is 2^(x log2e - c) in one fused operation, c an integer near
@@ -260,14 +254,14 @@ __device__ __forceinline__ double pow2(float k) {
     return k > -1000.0f ? __hiloint2double((1023 + (int)k) << 20, 0) : 0.0;
 }
 
-// A thread's largest logit and its sum of exponentials, in units of 2^c.
+// A lane's sum of exponentials, in units of 2^c.
 struct Running {
-    float m = -INFINITY, c = -2.0f * kMaxTop;
+    float c = -2.0f * kMaxTop;
     double sum = 0.0;
+    // adds a tile; returns its largest logit
     template <typename T>
-    __device__ __forceinline__ void add(const uint4 (&v)[VPT]) {
+    __device__ __forceinline__ float add(const uint4 (&v)[VPT]) {
         const float tm = Vec<T>::top(v);   // (NaN show in the sum)
-        m = fmaxf(m, tm);
         if (tm * kLog2e > c + kSpan) {
             const float up = ceilf(fminf(tm, kMaxTop) * kLog2e);
             sum *= pow2(c - up);
@@ -283,48 +277,54 @@ struct Running {
             }
         const float2 both = add2(s[0], s[1]);
         sum += (double)(both.x + both.y);
+        return tm;
     }
 };
 
 template <typename T>
-__global__ void __launch_bounds__(NT, 4) slice_kernel(const __grid_constant__ Args p) {
+__global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) slice_kernel(const __grid_constant__ Args p) {
     using X = Vec<T>;
-    constexpr int N = X::N, kStep = NT * N, kTile = kStep * VPT;
-    __shared__ float s_max[NT], s_c[NT / 32];
-    __shared__ double s_sum[NT / 32];
-    __shared__ int s_count[NT / 32];
-    __shared__ int s_list[NT];       // first elements of the threads that reach the bound
-    __shared__ uint64_t s_key[CAP];
-    __shared__ int s_listed, s_n;
-    __shared__ float s_bound;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int64_t row = blockIdx.x / (unsigned)p.slices;
-    const int slice = blockIdx.x % (unsigned)p.slices;
-    if (!row_live(p, row)) {
+    constexpr int N = X::N, kStep = 32 * N, kTile = kStep * VPT;
+    constexpr uint32_t kAll = 0xffffffffu;
+    __shared__ uint64_t s_keys[WARPS][CAP];
+    __shared__ float s_tops[WARPS][TILES * 32];
+    __shared__ uint16_t s_lists[WARPS][LISTED];
+    __shared__ int s_counts[WARPS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const unsigned at = blockIdx.x * WARPS + warp;
+    const unsigned row = at / (unsigned)p.slices, slice = at % (unsigned)p.slices;
+    if (at >= p.total || !row_live(p, row)) {
         grid_dependency_trigger();
         return;
     }
+    uint64_t* s_key = s_keys[warp];
+    float* s_top = s_tops[warp] + lane;   // this lane's largest logit of tile t: s_top[32 t]
+    uint16_t* s_list = s_lists[warp];
+    int& s_n = s_counts[warp];
     const T* x = static_cast<const T*>(p.logits) + row * p.ld;
-    const int first = slice * p.tiles * kTile + tid * N;   // this thread's first element
-    const int tiles = min(p.tiles, (p.V - slice * p.tiles * kTile + kTile - 1) / kTile);
     const int shift = (int)(reinterpret_cast<uintptr_t>(x) & 15u);
-
+    const int tile_lo = (int)((int64_t)p.tiles * slice / p.slices);
+    const int tiles = (int)((int64_t)p.tiles * (slice + 1) / p.slices) - tile_lo;
+    const int begin = tile_lo * kTile, first = begin + lane * N;   // this lane's first element
+    // lane's vector j of the slice, j < tiles * VPT
+    auto vec = [&](int j) { return load_vec<T>(x, first + j * kStep, p.V, shift); };
     auto load_tile = [&](uint4 (&u)[VPT], int t) {
         if (t >= tiles) return;
-        const int i0 = first + t * kTile, tile0 = (slice * p.tiles + t) * kTile;
-        if (shift == 0 && tile0 + kTile <= p.V) {
+        if (shift == 0 && begin + (t + 1) * kTile <= p.V) {
+            const T* at = x + first + t * kTile;
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) u[j] = ld_once(x + i0 + j * kStep);
+            for (int j = 0; j < VPT; ++j) u[j] = ld_once(at + j * kStep);
         } else {
 #pragma unroll 1
             for (int j = 0; j < VPT; ++j) {
-                const uint4 a = load_vec<T>(x, i0 + j * kStep, p.V, shift);
+                const uint4 a = vec(t * VPT + j);
 #pragma unroll
                 for (int k = 0; k < VPT; ++k)
                     if (k == j) u[k] = a;
             }
         }
     };
+
     // one tile's vectors are on their way while the other's are worked on
     uint4 even[VPT], odd[VPT];
     Running run;
@@ -332,109 +332,88 @@ __global__ void __launch_bounds__(NT, 4) slice_kernel(const __grid_constant__ Ar
 #pragma unroll 1
     for (int t = 0; t < tiles; t += 2) {
         load_tile(odd, t + 1);
-        run.add<T>(even);
+        s_top[32 * t] = run.template add<T>(even);
         if (t + 1 >= tiles) break;
         load_tile(even, t + 2);
-        run.add<T>(odd);
+        s_top[32 * t + 32] = run.template add<T>(odd);
     }
 
-    s_max[tid] = run.m;
-    if (tid == 0) {
-        s_listed = s_n = 0;
-        s_bound = -3.402823466e38f;
+    float mine[GROUPS], top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < GROUPS; ++i) {
+        mine[i] = -INFINITY;
+        for (int t = i; t < tiles; t += GROUPS) mine[i] = fmaxf(mine[i], s_top[32 * t]);   // (this lane's own)
+        top = fmaxf(top, mine[i]);
     }
     float c = run.c;
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, d));
+    for (int d = 16; d > 0; d >>= 1) {
+        top = fmaxf(top, __shfl_xor_sync(kAll, top, d));
+        c = fmaxf(c, __shfl_xor_sync(kAll, c, d));
+    }
     double sum = run.sum * pow2(run.c - c);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (lane == 0) {
-        s_sum[warp] = sum;
-        s_c[warp] = c;
-    }
-    __syncthreads();
-    float mine[NT / 32], top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < NT / 32; ++i) {
-        mine[i] = s_max[i * 32 + lane];
-        top = fmaxf(top, mine[i]);
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const bool redo_sum = top > -INFINITY && !(fabsf(top) <= kMaxTop);
-    const int finder = blockIdx.x % (NT / 32);   // (spreads this work over the schedulers)
-    if (warp == finder) {
-        float b;
-        if (find_bound(mine, top, p.n, &b) && lane == 0) s_bound = b;
-    } else if (warp == (finder + 1) % (NT / 32) && lane == 0 && !redo_sum) {
-        float most = s_c[0];
-        for (int i = 1; i < NT / 32; ++i) most = fmaxf(most, s_c[i]);
-        double t = 0.0;
-        for (int i = 0; i < NT / 32; ++i) t += s_sum[i] * pow2(s_c[i] - most);
-        p.stats[row * p.slices + slice] = Stat{t, most, top};
-    }
-    __syncthreads();
-    float bound = s_bound;
-    auto each_vec = [&](auto&& use) {   // use(vector, index) for the thread's vectors of the slice
-#pragma unroll 1
-        for (int t = 0; t < tiles; ++t)
-#pragma unroll 1
-            for (int j = 0; j < VPT; ++j) {
-                const int i0 = first + t * kTile + j * kStep;
-                use(load_vec<T>(x, i0, p.V, shift), i0);
-            }
-    };
-    if (redo_sum) {   // about the top itself
+    if (top > -INFINITY && !(fabsf(top) <= kMaxTop)) {
+        // beyond the fast sum: about the top itself
+        c = __int_as_float(0x7fffffff);
         sum = 0.0;
-        each_vec([&](uint4 u, int) {
+#pragma unroll 1
+        for (int j = 0; j < tiles * VPT; ++j) {
+            const uint4 u = vec(j);
             float part = 0.0f;
 #pragma unroll
             for (int e = 0; e < N; ++e) part += exp2_fast((X::get(u, e) - top) * kLog2e);
             sum += (double)part;
-        });
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (lane == 0) s_sum[warp] = sum;
-        __syncthreads();
-        if (tid == 0) {
-            double t = 0.0;
-            for (int i = 0; i < NT / 32; ++i) t += s_sum[i];
-            p.stats[row * p.slices + slice] = Stat{t, __int_as_float(0x7fffffff), top};
         }
     }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(kAll, sum, d);
+    if (lane == 0) {
+        p.stats[at] = Stat{sum, c, top};
+        s_n = 0;
+    }
 
-    // the threads that reach the bound, and of their vectors the logits that do
-    if (run.m >= bound) s_list[atomicAdd(&s_listed, 1)] = first;
-    __syncthreads();
-    const int per = tiles * VPT;
-    for (int i = tid; i < s_listed * per; i += NT) {
-        const int i0 = s_list[i / per] + i % per * kStep;   // (kTile is VPT kStep)
+    // the tile maxima that reach the bound, and of the vectors behind them the logits that do
+    float bound = find_bound(mine, top, p.n);
+    int listed = 0;
+#pragma unroll 4
+    for (int t = 0; t < tiles; ++t) {
+        const bool mine_hits = s_top[32 * t] >= bound;
+        const uint32_t hit = __ballot_sync(kAll, mine_hits);
+        const int k = listed + __popc(hit & ((1u << lane) - 1u));
+        if (mine_hits && k < LISTED) s_list[k] = (uint16_t)(t * 32 + lane);
+        listed += __popc(hit);
+    }
+    __syncwarp();
+    for (int i = lane; i < min(listed, LISTED) * VPT; i += 32) {
+        const int set = s_list[i / VPT];
+        const int i0 = begin + set / 32 * kTile + i % VPT * kStep + set % 32 * N;
         const uint4 u[1] = {load_vec<T>(x, i0, p.V, shift)};
         if (X::top(u) >= bound) {
 #pragma unroll
             for (int e = 0; e < N; ++e) {
                 const float f = X::get(u[0], e);
                 if (f >= bound) {
-                    const int at = atomicAdd(&s_n, 1);
-                    if (at < CAP) s_key[at] = make_key(f, i0 + e);
+                    const int k = atomicAdd(&s_n, 1);
+                    if (k < CAP) s_key[k] = make_key(f, i0 + e);
                 }
             }
         }
     }
-    __syncthreads();
-    if (s_n > CAP) {
+    __syncwarp();
+    if (listed > LISTED || s_n > CAP) {
         // Too many reach it.  The n-th largest logit itself ...
-        auto each = [&](auto&& use) {   // use(value, index)
-            each_vec([&](uint4 u, int i0) {
+        auto each = [&](auto&& use) {   // use(value, index) for the lane's logits
+#pragma unroll 1
+            for (int j = 0; j < tiles * VPT; ++j) {
+                const uint4 u = vec(j);
 #pragma unroll
-                for (int e = 0; e < N; ++e) use(X::get(u, e), i0 + e);
-            });
+                for (int e = 0; e < N; ++e) use(X::get(u, e), first + j * kStep + e);
+            }
         };
         auto count = [&](auto&& pred) {
             int n = 0;
             each([&](float f, int i) { n += pred(f, i); });
-            return block_count(n, s_count);
+            return __reduce_add_sync(kAll, n);
         };
         uint32_t lo = ordered(bound), hi = ordered(top);
         while (hi > lo) {
@@ -446,29 +425,31 @@ __global__ void __launch_bounds__(NT, 4) slice_kernel(const __grid_constant__ Ar
         bound = from_ordered(lo);
         // ... and the index of the last one of its kind that is still among the n
         const int above = count([&](float f, int) { return f > bound; });
-        int i_lo = slice * p.tiles * kTile, i_hi = min(p.V, i_lo + tiles * kTile) - 1;
+        int i_lo = begin, i_hi = min(p.V, begin + tiles * kTile) - 1;
         while (i_lo < i_hi) {
             const int mid = i_lo + (i_hi - i_lo) / 2;
             if (above + count([&](float f, int i) { return f == bound && i <= mid; }) >= p.n) i_hi = mid;
             else i_lo = mid + 1;
         }
-        if (tid == 0) s_n = 0;
-        __syncthreads();
+        __syncwarp();
+        if (lane == 0) s_n = 0;
+        __syncwarp();
         each([&](float f, int i) {
             if (f > bound || (f == bound && i <= i_lo)) s_key[atomicAdd(&s_n, 1)] = make_key(f, i);
         });
-        __syncthreads();
+        __syncwarp();
     }
-    grid_dependency_trigger();   // (the merge may be set up; it waits for this grid's end)
     const int total = s_n;
-    uint64_t* out = p.cand + (row * p.slices + slice) * p.n;
-    for (int i = tid; i < total; i += NT) {
+    uint64_t* out = p.cand + (int64_t)at * p.n;
+    for (int i = lane; i < total; i += 32) {
         const uint64_t k = s_key[i];
         int rank = 0;
+#pragma unroll 4
         for (int j = 0; j < total; ++j) rank += s_key[j] > k;
         if (rank < p.n) out[rank] = k;
     }
-    for (int i = total + tid; i < p.n; i += NT) out[i] = 0;
+    for (int i = total + lane; i < p.n; i += 32) out[i] = 0;
+    grid_dependency_trigger();   // (the merge may be set up; it waits for this grid's end)
 }
 
 // fp64 scores in order as unsigned integers (never 0 for a finite one).
@@ -484,7 +465,7 @@ __device__ __forceinline__ double from_ordered64(uint64_t k) {
 struct Cand {
     uint64_t score;   // ordered; 0: none
     uint32_t at;      // w * V + v
-    uint32_t unused;
+    uint32_t rough;   // the score rounded down to fp32, ordered; 0: none
 };
 __device__ __forceinline__ bool better(const Cand& a, const Cand& b) {
     return a.score > b.score || (a.score == b.score && a.at < b.at);
@@ -510,16 +491,65 @@ __device__ __forceinline__ void rank_all(const Cand* c, int total, F&& use) {
     }
 }
 
+// A bound on the rough scores that at least n of c[0 .. total) reach and not many more
+// (n + 8, but for equal ones); 1, which all candidates reach, where there are no more than
+// n.  By the whole block; s is scratch in shared memory that nothing else uses.
+struct Scratch {
+    int valid;
+    uint32_t least, most;
+};
+__device__ __noinline__ uint32_t block_bound(const Cand* c, int total, int n, Scratch* s) {
+    const int tid = threadIdx.x;
+    if (tid == 0) *s = Scratch{0, ~0u, 0};
+    __syncthreads();
+    uint32_t least = ~0u, most = 0;
+    int valid = 0;
+    for (int i = tid; i < total; i += MT) {
+        const uint32_t r = c[i].rough;
+        if (r) {
+            ++valid;
+            least = min(least, r);
+            most = max(most, r);
+        }
+    }
+    valid = __reduce_add_sync(0xffffffffu, valid);
+    least = __reduce_min_sync(0xffffffffu, least);
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (tid % 32 == 0) {
+        atomicAdd(&s->valid, valid);
+        atomicMin(&s->least, least);
+        atomicMax(&s->most, most);
+    }
+    __syncthreads();
+    int reach = s->valid;
+    if (reach <= n) return 1;
+    uint32_t lo = s->least, hi = s->most;   // at least n reach lo, fewer reach anything above hi
+    while (reach > n + 8 && hi > lo) {
+        const uint32_t mid = lo + (hi - lo + 1) / 2;
+        int k = 0;
+        for (int i = 0; i < total; i += MT) k += __syncthreads_count(i + tid < total && c[i + tid].rough >= mid);
+        if (k >= n) {
+            lo = mid;
+            reach = k;
+        } else {
+            hi = mid - 1;
+        }
+    }
+    return lo;
+}
+
 // Shared memory of a merge block: list heads, candidates, then the group's keys if they
 // are held there (up to kMaxKeyBytes).
 constexpr size_t kMaxKeyBytes = 64 * 1024;
+constexpr int kFew = 96;               // candidates that are ranked as they are
 constexpr int kMaxLists = 4096;        // of a group
 constexpr size_t kMaxMergeSmem = (kMaxLists + (size_t)kMaxOut * kMaxOut) * sizeof(Cand) + kMaxKeyBytes;
 static_assert(kMaxMergeSmem <= 225 * 1024, "shared memory of the merge");
+__host__ __device__ constexpr int merge_cap(int n) { return n * n < 512 ? 512 : n * n; }   // candidates
 inline size_t merge_key_bytes(int W, int slices, int n) { return (size_t)W * slices * n * sizeof(uint64_t); }
 inline size_t merge_smem(int W, int slices, int n) {
     const size_t keys = merge_key_bytes(W, slices, n);
-    return ((size_t)W * slices + (size_t)n * n) * sizeof(Cand) + (keys <= kMaxKeyBytes ? keys : 0);
+    return ((size_t)W * slices + merge_cap(n)) * sizeof(Cand) + (keys <= kMaxKeyBytes ? keys : 0);
 }
 
 // One block per group.
@@ -531,16 +561,17 @@ __global__ void __launch_bounds__(MT) merge_kernel(const __grid_constant__ Args 
     __shared__ double ref[kMaxBeams], offset[kMaxBeams];
     __shared__ uint8_t kind[kMaxBeams];    // 0: no candidates, 1: from the logits, 2: finished
     __shared__ int sel[kMaxOut];           // the lists of the n best heads, best first
-    __shared__ int s_n;
+    __shared__ int s_n, s_few;
+    __shared__ Scratch scratch[2];
+    __shared__ Cand few[kFew];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row0 = (int64_t)blockIdx.x * p.W;
     const int lists = p.W * p.slices;
-    if (tid < kMaxOut) sel[tid] = -1;
-    if (tid == 0) s_n = 0;
+    if (tid == 0) s_n = s_few = 0;
     grid_dependency_wait();
     const uint64_t* keys = p.cand + row0 * p.slices * p.n;
     if (p.keys_in_smem) {   // (of rows that left none too: whatever is there is not used)
-        uint64_t* mine = reinterpret_cast<uint64_t*>(cand + p.n * p.n);
+        uint64_t* mine = reinterpret_cast<uint64_t*>(cand + merge_cap(p.n));
         for (int i = tid; i < lists * p.n; i += MT) mine[i] = keys[i];
         keys = mine;
     }
@@ -593,43 +624,73 @@ __global__ void __launch_bounds__(MT) merge_kernel(const __grid_constant__ Args 
     // the first of its first list.
     auto entry = [&](int l, int e) {
         const int w = l / p.slices;
-        Cand c{0, 0, 0};
+        double score = offset[w];
+        Cand c{0, (uint32_t)w * p.V + p.pad, 0};
         if (kind[w] == 1) {
             const uint64_t k = keys[l * p.n + e];
-            if (k) {
-                c.score = ordered64(((double)from_ordered((uint32_t)(k >> 32)) - ref[w]) + offset[w]);
-                c.at = (uint32_t)w * p.V + (0xffffffffu - (uint32_t)k);
-            }
-        } else if (kind[w] == 2 && l % p.slices == 0 && e == 0) {
-            c.score = ordered64(offset[w]);
-            c.at = (uint32_t)w * p.V + p.pad;
+            if (!k) return c;
+            score += (double)from_ordered((uint32_t)(k >> 32)) - ref[w];
+            c.at = (uint32_t)w * p.V + (0xffffffffu - (uint32_t)k);
+        } else if (kind[w] == 0 || l % p.slices != 0 || e != 0) {
+            return c;
         }
+        c.score = ordered64(score);
+        c.rough = ordered(__double2float_rd(score));
         return c;
     };
+    // What n heads reach, the n best candidates reach: they are collected, a warp to a list,
+    // and narrowed down once more, since one beam's may be most of them.
     for (int l = tid; l < lists; l += MT) head[l] = entry(l, 0);
     __syncthreads();
-
-    // The n best heads: the n best candidates are in their lists, at or above the n-th of them.
-    rank_all(head, lists, [&](int l, int rank) {
-        if (rank < p.n && head[l].score) sel[rank] = l;
-    });
-    __syncthreads();
-    // (fewer lists than results: no bound)
-    const Cand least = sel[p.n - 1] < 0 ? Cand{0, 0xffffffffu, 0} : head[sel[p.n - 1]];
-    for (int i = tid; i < p.n * p.n; i += MT) {
-        const int l = sel[i / p.n];
-        if (l < 0) continue;
-        const Cand c = entry(l, i % p.n);
-        if (c.score && !better(least, c)) cand[atomicAdd(&s_n, 1)] = c;
+    const uint32_t bound = block_bound(head, lists, p.n, &scratch[0]);
+    for (int l = warp; l < lists; l += MT / 32) {
+        if (head[l].rough < bound) continue;
+        for (int e = lane; e < p.n; e += 32) {
+            const Cand c = entry(l, e);
+            if (c.rough >= bound) {
+                const int k = atomicAdd(&s_n, 1);
+                if (k < merge_cap(p.n)) cand[k] = c;
+            }
+        }
     }
     __syncthreads();
-    const int total = s_n;
+    if (s_n > merge_cap(p.n)) {
+        // Ties make them too many: from the lists of exactly the n best heads, what is not
+        // behind the n-th of them.
+        rank_all(head, lists, [&](int l, int rank) {
+            if (rank < p.n && head[l].score) sel[rank] = l;
+        });
+        __syncthreads();
+        if (tid == 0) s_n = 0;
+        const Cand last = head[sel[p.n - 1]];
+        __syncthreads();
+        for (int i = tid; i < p.n * p.n; i += MT) {
+            const Cand c = entry(sel[i / p.n], i % p.n);
+            if (c.score && !better(last, c)) cand[atomicAdd(&s_n, 1)] = c;
+        }
+        __syncthreads();
+    }
+    int total = s_n;
+    const Cand* from = cand;
+    if (total > kFew) {
+        const uint32_t closer = block_bound(cand, total, p.n, &scratch[1]);
+        for (int i = tid; i < total; i += MT)
+            if (cand[i].rough >= closer) {
+                const int k = atomicAdd(&s_few, 1);
+                if (k < kFew) few[k] = cand[i];
+            }
+        __syncthreads();
+        if (s_few <= kFew) {   // (else: ties)
+            from = few;
+            total = s_few;
+        }
+    }
     const int64_t out = (int64_t)blockIdx.x * p.n;
-    rank_all(cand, total, [&](int i, int rank) {
+    rank_all(from, total, [&](int i, int rank) {
         if (rank >= p.n) return;
-        p.parents[out + rank] = (int32_t)(cand[i].at / (uint32_t)p.V);
-        p.tokens[out + rank] = (int32_t)(cand[i].at % (uint32_t)p.V);
-        p.out_scores[out + rank] = (float)from_ordered64(cand[i].score);
+        p.parents[out + rank] = (int32_t)(from[i].at / (uint32_t)p.V);
+        p.tokens[out + rank] = (int32_t)(from[i].at % (uint32_t)p.V);
+        p.out_scores[out + rank] = (float)from_ordered64(from[i].score);
     });
     for (int i = total + tid; i < p.n; i += MT) {
         p.parents[out + i] = -1;

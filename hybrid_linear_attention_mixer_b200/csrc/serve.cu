@@ -287,7 +287,8 @@ gdn_status run_linear_i8(const void* x, int32_t x_dtype, const float* x_scale, c
 // ---------------------------------------------------------------------------
 // Beam selection
 // ---------------------------------------------------------------------------
-constexpr int kBeamTiles = 8, kBeamWaves = 6;
+constexpr int kBeamTiles = 4;
+constexpr int kBeamWarps = 148 * 32;    // the slice warps that the GPU holds
 
 struct BeamLayout {
     int slices, tiles;
@@ -299,16 +300,22 @@ gdn_status beam_layout(int32_t n_groups, int32_t n_beams, int32_t vocab, int32_t
     if (n_groups < 0 || n_beams <= 0 || vocab <= 0 || n_out <= 0 || !float_dtype(dtype)) return GDN_ERR_INVALID_ARG;
     if (n_beams > GDN_BEAM_MAX_BEAMS || n_out > GDN_BEAM_MAX_OUT || vocab > GDN_BEAM_MAX_VOCAB)
         return GDN_ERR_UNSUPPORTED;
-    // Tiles of a slice: enough slices for several waves of blocks, then longer ones, whose
-    // selection costs less per logit.
-    const int tile = gdn::beam::tile_len(elem(dtype)), row_tiles = (vocab + tile - 1) / tile;
-    const int64_t waves = (int64_t)n_groups * n_beams * row_tiles / (kBeamWaves * 4 * 148);
-    L->tiles = (int)std::min<int64_t>(std::max<int64_t>(waves, 1), kBeamTiles);
+    // Tiles of a slice: at least kBeamTiles (shorter ones spend more on their selection and
+    // leave the merge more lists) and n / 16 (a tile has 32 maxima for n of them to be
+    // among); longer ones where the slices fill the GPU's warps anyway.
+    const int len = gdn::beam::tile_len(elem(dtype));
+    L->tiles = (vocab + len - 1) / len;
+    const int64_t rows = std::max<int64_t>((int64_t)n_groups * n_beams, 1);
+    int64_t each = std::max<int64_t>(rows * L->tiles / kBeamWarps + 1, std::max(kBeamTiles, (n_out + 15) / 16));
+    each = std::min<int64_t>(each, gdn::beam::TILES);
+    L->slices = std::max((int)(L->tiles / each), 1);
+    L->slices = std::max(L->slices, (L->tiles + gdn::beam::TILES - 1) / gdn::beam::TILES);
     // (a merge block holds a list head per slice of the group)
-    while ((int64_t)n_beams * ((row_tiles + L->tiles - 1) / L->tiles) > gdn::beam::kMaxLists) ++L->tiles;
-    L->slices = (row_tiles + L->tiles - 1) / L->tiles;
+    L->slices = std::min(L->slices, gdn::beam::kMaxLists / n_beams);
+    static_assert(GDN_BEAM_MAX_VOCAB / gdn::beam::tile_len(4) <= gdn::beam::kMaxLists / GDN_BEAM_MAX_BEAMS * gdn::beam::TILES,
+                  "tiles of a slice");
     const int64_t lists = (int64_t)n_groups * n_beams * L->slices;
-    if (lists > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;   // one block each
+    if (lists > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;   // (their numbers are 32 bits)
     L->cand_off = align_up((size_t)lists * sizeof(gdn::beam::Stat), 256);
     L->total = L->cand_off + align_up((size_t)lists * n_out * sizeof(uint64_t), 256);
     return GDN_OK;
@@ -510,9 +517,10 @@ gdn_status gdn_beam_select(const void* logits, int32_t logits_dtype, int64_t ld,
     a.tokens = tokens;
     a.out_scores = out_scores;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const unsigned grid = (unsigned)(rows * L.slices);
-    if (logits_dtype == GDN_BF16) gdn::beam::slice_kernel<__nv_bfloat16><<<grid, gdn::beam::NT, 0, st>>>(a);
-    else gdn::beam::slice_kernel<float><<<grid, gdn::beam::NT, 0, st>>>(a);
+    a.total = (unsigned)(rows * L.slices);
+    const unsigned grid = (a.total + gdn::beam::WARPS - 1) / gdn::beam::WARPS, block = 32 * gdn::beam::WARPS;
+    if (logits_dtype == GDN_BF16) gdn::beam::slice_kernel<__nv_bfloat16><<<grid, block, 0, st>>>(a);
+    else gdn::beam::slice_kernel<float><<<grid, block, 0, st>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_status(e);
     e = allow_smem<gdn::beam::merge_kernel>(gdn::beam::kMaxMergeSmem);
