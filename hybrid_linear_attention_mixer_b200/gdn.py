@@ -157,8 +157,23 @@ def status_string(s: int) -> str:
     return lib().gdn_status_string(int(s)).decode()
 
 
+class _Fields:
+    """A dataclass whose C struct is made once and again after a field is set."""
+
+    def __setattr__(self, name, value):
+        self.__dict__.pop("_made", None)
+        object.__setattr__(self, name, value)
+
+    def ref(self):
+        """A pointer to the C struct, for a call."""
+        made = self.__dict__.get("_made")
+        if made is None:
+            made = self.__dict__["_made"] = ctypes.byref(self.c())
+        return made
+
+
 @dataclass
-class Config:
+class Config(_Fields):
     """Layer shape; the defaults are the published layer (16 / 48 heads of 128, K = 4)."""
     n_k_heads: int = 16
     n_v_heads: int = 48
@@ -433,26 +448,31 @@ def _device_of(t, name):
 
 def _shaped(t, name, dtype, device, *shape):
     """A contiguous tensor of this dtype, device and shape: its address."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device.index and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError("%s: dtype %s, expected %s" % (name, t.dtype, dtype))
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), shape))
     if t.device != device:
         raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr()
+    raise ValueError("%s must be contiguous" % name)
+
+
+# The current stream's handle by device index: the binding's own lookup where torch has it
+# (a Stream object costs several times as much to make as the call's other arguments).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _call(fn, what, device, stream, *args):
     """fn(*args, stream) on the tensors' device, which need not be the current one.  The
     stream is the caller's, else that device's current one."""
-    if torch.cuda.current_device() != device.index:
+    if _current_device() != device.index:
         with torch.cuda.device(device):
             return _call(fn, what, device, stream, *args)
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    s = fn(*args, stream.cuda_stream)
+    s = fn(*args, _raw_stream(device.index) if stream is None else stream.cuda_stream)
     if s != 0:
         raise GdnError(s, what)
 
@@ -471,7 +491,7 @@ _GATE_ACTS = {"linear": 0, "sigmoid": 1}
 
 
 @dataclass
-class NormConfig:
+class NormConfig(_Fields):
     """The norms between two blocks (block_norm)."""
     dim: int = 2560
     eps: float = 1e-6
@@ -530,7 +550,7 @@ def block_norm(cfg: NormConfig, o, x, gate=None, w_post=None, w_pre=None, r=None
         py = _shaped(y, "y", y_dtype, dev, T, D)
     elif y is not None or y_scale is not None or quantize:
         raise ValueError("y without w_pre")
-    _call(lib().gdn_block_norm, "gdn_block_norm", dev, stream, ctypes.byref(cfg.c()), po, px, pg, pp, pw, T, pr, py, ps)
+    _call(lib().gdn_block_norm, "gdn_block_norm", dev, stream, cfg.ref(), po, px, pg, pp, pw, T, pr, py, ps)
     return r, y, y_scale
 
 
@@ -577,7 +597,7 @@ def _i8_operand(x, x_scale, name, dev, M, K, workspace, stream):
 
 
 def _workspace(t, dev):
-    if t.dtype != torch.uint8 or t.device != dev or not t.is_contiguous():
+    if t.dtype is not torch.uint8 or t.get_device() != dev.index or not t.is_contiguous():
         raise ValueError("workspace must be contiguous uint8 on %s" % dev)
     return t.data_ptr()
 
@@ -624,14 +644,15 @@ def in_proj_i8(cfg: Config, hidden, w_in, w_scale, hidden_scale=None, out: dict 
     pw, pws = _shaped(w_in, "w_in", torch.int8, dev, N, D), _shaped(w_scale, "w_scale", torch.float32, dev, N)
     o = out if out is not None else {n: _empty((T, wd), torch.bfloat16, dev, stream) for n, wd in widths}
     ptrs = []
-    for n, wd in widths:
+    for n, wd in widths:   # (flat or by heads, as for in_proj)
         t = o[n]
-        _check(t, n, torch.bfloat16, dev)
+        if t.dtype is not torch.bfloat16 or t.get_device() != dev.index or not t.is_contiguous():
+            _check(t, n, torch.bfloat16, dev)
         if t.numel() != T * wd:
             raise ValueError("%s must hold [T, %d]" % (n, wd))
         ptrs.append(t.data_ptr())
     px, xdt, pxs, ws, ws_bytes, workspace = _i8_operand(hidden, hidden_scale, "hidden", dev, T, D, workspace, stream)
-    _call(lib().gdn_in_proj_i8, "gdn_in_proj_i8", dev, stream, ctypes.byref(cfg.c()), px, xdt, pxs, pw, pws, T, D,
+    _call(lib().gdn_in_proj_i8, "gdn_in_proj_i8", dev, stream, cfg.ref(), px, xdt, pxs, pw, pws, T, D,
           *ptrs, ws, ws_bytes)
     return o
 
@@ -645,7 +666,7 @@ def out_proj_i8(cfg: Config, o, w_out, w_scale, o_scale=None, y=None, workspace=
     if y is None:
         y = _empty((T, D), torch.bfloat16, dev, stream)
     px, xdt, pxs, ws, ws_bytes, workspace = _i8_operand(o2, o_scale, "o", dev, T, K, workspace, stream)
-    _call(lib().gdn_out_proj_i8, "gdn_out_proj_i8", dev, stream, ctypes.byref(cfg.c()), px, xdt, pxs,
+    _call(lib().gdn_out_proj_i8, "gdn_out_proj_i8", dev, stream, cfg.ref(), px, xdt, pxs,
           _shaped(w_out, "w_out", torch.int8, dev, D, K), _shaped(w_scale, "w_scale", torch.float32, dev, D), T, D,
           _shaped(y, "y", torch.bfloat16, dev, T, D), ws, ws_bytes)
     return y
