@@ -265,7 +265,7 @@ linear_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ 
 //                loads complete on it (the .cta_group::2 form of the load)
 //   empty[s]     in each CTA: one commit from CTA 0's MMA thread per CTA
 //   acc_full[a]  in each CTA: one commit per CTA when a tile's MMAs are done
-//   acc_empty[a] in CTA 0: 4 epilogue warps x 2 CTAs arrive (cluster scope)
+//   acc_empty[a] in CTA 0: the epilogue warps of both CTAs arrive (cluster scope)
 // No load is multicast; every cross-CTA signal names one barrier.
 // ---------------------------------------------------------------------------
 template <int BN>
@@ -352,18 +352,24 @@ struct Bf16Op {
     using Args = gemm::Args;
     static constexpr int BK = gemm::BK;
     static constexpr bool kAfterQuantize = false;
+    static constexpr int kEpiWarps = 4;        // epilogue warps: 4, or 8 with half the columns each
+    static constexpr int kEpiSmem = 0;         // bytes of shared memory the epilogue wants
     static __host__ __device__ constexpr uint32_t idesc(int M, int N) { return idesc_bf16(M, N); }
     static __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
         mma_pair_w(d, a, b, id, acc);
     }
+    // what the epilogue can do before the accumulator is there
     template <int BN>
-    static __device__ __forceinline__ void store(uint32_t taddr, const Args& p, int64_t m, int n0) {
+    static __device__ __forceinline__ float prepare(const Args&, int64_t, int, int, int, void*) { return 0.0f; }
+    // row m of the tile, columns [n0, n0 + BN) (of 8 warps: part 0 or 1 of them)
+    template <int BN>
+    static __device__ __forceinline__ void store(uint32_t taddr, const Args& p, int64_t m, int n0, int, float, void*) {
         store_row<BN>(taddr, p, m, n0);
     }
 };
 
 template <int BN, class Op = Bf16Op>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NT, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(64 + 32 * Op::kEpiWarps, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                    const __grid_constant__ typename Op::Args p) {
     using S = Shape2<BN>;
@@ -391,7 +397,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(acc_full(a), 1);
-            mbar_init(acc_empty(a), 8);
+            mbar_init(acc_empty(a), 2 * Op::kEpiWarps);
         }
         mbar_init(drain, 1);
         *s_abort = 0;
@@ -493,20 +499,22 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
         }
     } else {
         // ---- epilogue: this CTA's 128 rows of the pair tile ----
-        const int q = warp & 3;
+        const int q = warp & 3, part = (warp - 2) >> 2;
         const int row = q * 32 + lane;
+        void* own = smem + ((S::SMEM_USED + 15) & ~15) + (warp - 2) * (Op::kEpiSmem / Op::kEpiWarps);
         uint32_t ti = 0;
         bool ok = true;
         for (int64_t t = pair; t < tiles; t += n_pairs, ++ti) {
             const uint32_t a = ti & 1u;
+            const int mb = (int)(t % m_pairs), nb = (int)(t / m_pairs);
+            const int64_t m = (int64_t)mb * 2 * BM + (int64_t)rank * BM + row;
+            const float xs = Op::template prepare<BN>(p, m, nb * BN, part, lane, own);
             if (!mbar_wait_bounded(acc_full(a), (ti >> 1) & 1u) || *s_abort) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            const int mb = (int)(t % m_pairs), nb = (int)(t / m_pairs);
-            Op::template store<BN>(tmem + ((uint32_t)(q * 32) << 16) + a * BN, p,
-                                   (int64_t)mb * 2 * BM + (int64_t)rank * BM + row, nb * BN);
+            Op::template store<BN>(tmem + ((uint32_t)(q * 32) << 16) + a * BN, p, m, nb * BN, part, xs, own);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_cluster(map_to_rank(acc_empty(a), 0));

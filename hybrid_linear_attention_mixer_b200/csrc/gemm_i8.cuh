@@ -60,11 +60,27 @@ struct I8Op {
     static __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
         mma_i8_pair_w(d, a, b, id, acc);
     }
+    // A tile's main loop is half as long as the bf16 form's, so its epilogue has half the
+    // time: twice the warps, and the scales fetched while the accumulator is still at work.
+    static constexpr int kEpiWarps = 8;
+    static constexpr int kEpiSmem = 8 * 128 * 4;   // w_scale of a warp's up to four 32-column chunks
+    template <int BN>
+    static __device__ __forceinline__ float prepare(const Args& p, int64_t m, int n0, int part, int lane, void* own) {
+        float* ws = static_cast<float*>(own);
+        __syncwarp();   // (the tile before this one is done with ws)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = part + 2 * i, n = n0 + c * 32 + lane;
+            if (c < BN / 32) ws[i * 32 + lane] = n < p.N ? __ldg(p.w_scale + n) : 0.0f;
+        }
+        __syncwarp();
+        return m < p.M ? p.x_scale[m] : 0.0f;
+    }
     // Eight columns of row m, scaled: a segment is a multiple of 8 wide.
-    static __device__ __forceinline__ void store8(const uint32_t* r, const Args& p, int64_t m, int n8, float xs) {
+    static __device__ __forceinline__ void store8(const uint32_t* r, const float* ws, const Args& p, int64_t m, int n8,
+                                                  float xs) {
         if (n8 >= p.N || m >= p.M) return;
-        const float4 w0 = __ldg(reinterpret_cast<const float4*>(p.w_scale + n8));
-        const float4 w1 = __ldg(reinterpret_cast<const float4*>(p.w_scale + n8) + 1);
+        const float4 w0 = reinterpret_cast<const float4*>(ws)[0], w1 = reinterpret_cast<const float4*>(ws)[1];
         const float w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
         float f[8];
 #pragma unroll
@@ -83,14 +99,16 @@ struct I8Op {
         }
     }
     template <int BN>
-    static __device__ __forceinline__ void store(uint32_t taddr, const Args& p, int64_t m, int n0) {
-        const float xs = m < p.M ? p.x_scale[m] : 0.0f;
+    static __device__ __forceinline__ void store(uint32_t taddr, const Args& p, int64_t m, int n0, int part, float xs,
+                                                 void* own) {
+        const float* ws = static_cast<const float*>(own);
 #pragma unroll 1
-        for (int c = 0; c < BN / 32; ++c) {
+        for (int i = 0; 2 * i + part < BN / 32; ++i) {
+            const int c = 2 * i + part;
             uint32_t r[32];
             tmem_ld32(taddr + c * 32, r);
 #pragma unroll
-            for (int g = 0; g < 4; ++g) store8(r + 8 * g, p, m, n0 + c * 32 + g * 8, xs);
+            for (int g = 0; g < 4; ++g) store8(r + 8 * g, ws + i * 32 + g * 8, p, m, n0 + c * 32 + g * 8, xs);
         }
     }
 };

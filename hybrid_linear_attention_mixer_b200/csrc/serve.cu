@@ -139,13 +139,13 @@ bool i8_map(CUtensorMap* m, const void* base, int64_t rows, int K, int box_rows)
 // Clusters of `size` CTAs of a kernel that the device holds at once, asked of the
 // runtime once per device and size.
 template <auto Kernel>
-int resident_clusters(int size, size_t smem) {
+int resident_clusters(int size, unsigned threads, size_t smem) {
     static int known[64][4];
     int dev = 0, n = 0;
     const int slot = size == 1 ? 0 : size == 2 ? 1 : size == 4 ? 2 : 3;
     if (cudaGetDevice(&dev) != cudaSuccess) return 1;
     if (dev < 64 && known[dev][slot]) return known[dev][slot];
-    Launch l((unsigned)(sm_count() / size * size), gdn::gemm::NT, smem, nullptr);
+    Launch l((unsigned)(sm_count() / size * size), threads, smem, nullptr);
     l.cluster((unsigned)size);
     if (size == 1) n = sm_count();
     else if (cudaOccupancyMaxActiveClusters(&n, Kernel, &l.cfg) != cudaSuccess || n <= 0) {
@@ -159,15 +159,19 @@ int resident_clusters(int size, size_t smem) {
 template <int BN>
 cudaError_t launch_i8_pair(const void* x, const void* w, gdn::gemm::I8Args a, bool behind_quantize, cudaStream_t st) {
     using S = gdn::gemm::Shape2<BN>;
-    constexpr auto kernel = gdn::gemm::linear_pair_kernel<BN, gdn::gemm::I8Op>;
+    using Op = gdn::gemm::I8Op;
+    constexpr auto kernel = gdn::gemm::linear_pair_kernel<BN, Op>;
+    constexpr unsigned threads = 64 + 32 * Op::kEpiWarps;
+    constexpr size_t smem = S::SMEM + 16 + Op::kEpiSmem;
+    static_assert(smem <= 227 * 1024, "shared memory");
     CUtensorMap tm_x, tm_w;
     if (!i8_map(&tm_x, x, a.M, a.K, gdn::gemm::BM) || !i8_map(&tm_w, w, a.N, a.K, BN / 2)) return cudaErrorInvalidValue;
     a.n_blocks = (a.N + BN - 1) / BN;
     a.tiles = (a.M + 2 * gdn::gemm::BM - 1) / (2 * gdn::gemm::BM) * a.n_blocks;
-    cudaError_t e = allow_smem<kernel>(S::SMEM);
+    cudaError_t e = allow_smem<kernel>(smem);
     if (e != cudaSuccess) return e;
-    const int pairs = (int)std::min<int64_t>(a.tiles, resident_clusters<kernel>(2, S::SMEM));
-    Launch l((unsigned)(2 * pairs), gdn::gemm::NT, S::SMEM, st);   // (the kernel names its cluster size)
+    const int pairs = (int)std::min<int64_t>(a.tiles, resident_clusters<kernel>(2, threads, smem));
+    Launch l((unsigned)(2 * pairs), threads, smem, st);   // (the kernel names its cluster size)
     l.overlapped(behind_quantize);
     return cudaLaunchKernelEx(&l.cfg, kernel, tm_x, tm_w, a);
 }
@@ -205,7 +209,7 @@ cudaError_t launch_i8_rows(const void* x, const void* w, gdn::gemm::I8Args a, bo
     int splits = 1;
     int64_t best = -1;
     for (int s = 1; s <= 8 && s <= kb; s *= 2) {
-        const int at_once = resident_clusters<kernel>(s, S::SMEM);
+        const int at_once = resident_clusters<kernel>(s, gdn::gemm::NT, S::SMEM);
         if (s > 1 && a.n_blocks > at_once) break;   // one tile per cluster
         const int64_t cost = (int64_t)((a.n_blocks + at_once - 1) / at_once) * ((kb + s - 1) / s) + (s > 1 ? 4 : 0);
         if (best < 0 || cost < best) {
