@@ -291,6 +291,7 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) slice_kernel(const __g
     __shared__ uint16_t s_lists[WARPS][LISTED];
     __shared__ int s_counts[WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    grid_dependency_wait();
     const unsigned at = blockIdx.x * WARPS + warp;
     const unsigned row = at / (unsigned)p.slices, slice = at % (unsigned)p.slices;
     if (at >= p.total || !row_live(p, row)) {
@@ -568,6 +569,7 @@ __global__ void __launch_bounds__(MT) merge_kernel(const __grid_constant__ Args 
     const int64_t row0 = (int64_t)blockIdx.x * p.W;
     const int lists = p.W * p.slices;
     if (tid == 0) s_n = s_few = 0;
+    grid_dependency_trigger();
     grid_dependency_wait();
     const uint64_t* keys = p.cand + row0 * p.slices * p.n;
     if (p.keys_in_smem) {   // (of rows that left none too: whatever is there is not used)

@@ -107,6 +107,8 @@ __global__ void __launch_bounds__(WARPS * 32) block_norm_kernel(const __grid_con
     constexpr int NT = WARPS * 32;
     __shared__ float slot_o[WARPS], slot_r[WARPS];
     __shared__ uint32_t slot_y[WARPS];
+    grid_dependency_trigger();
+    grid_dependency_wait();
     const int64_t row = blockIdx.x, base = row * p.D;
     const int nv = p.D / 8;
     const TA* o = static_cast<const TA*>(p.o);

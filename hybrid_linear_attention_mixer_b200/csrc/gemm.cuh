@@ -351,7 +351,7 @@ __device__ __forceinline__ void commit_pair_w(uint32_t bar) {
 struct Bf16Op {
     using Args = gemm::Args;
     static constexpr int BK = gemm::BK;
-    static constexpr bool kAfterQuantize = false;
+    static constexpr bool kOverlapped = false;   // launched to overlap the kernel before it
     static constexpr int kEpiWarps = 4;        // epilogue warps: 4, or 8 with half the columns each
     static constexpr int kEpiSmem = 0;         // bytes of shared memory the epilogue wants
     static __host__ __device__ constexpr uint32_t idesc(int M, int N) { return idesc_bf16(M, N); }
@@ -415,7 +415,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_consta
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
     // x and its scales may still be on their way from the kernel before this one
-    if constexpr (Op::kAfterQuantize) grid_dependency_wait();
+    if constexpr (Op::kOverlapped) {
+        grid_dependency_trigger();
+        grid_dependency_wait();
+    }
     const int kb_n = (p.K + BK - 1) / BK;
     const int64_t m_pairs = (p.M + 2 * BM - 1) / (2 * BM);
     const int64_t tiles = m_pairs * p.n_blocks;

@@ -26,6 +26,7 @@ struct I8Args : Args {
     const float* x_scale;
     const float* w_scale;
     int out_f32;           // destinations are fp32 (else bf16)
+    int w_ready;           // the kernel before this one does not write w
 };
 
 #define GDN_ELECT "{\n\t.reg .pred e;\n\t.reg .b32 ex;\n\telect.sync ex|e, 0xffffffff;\n\t"
@@ -55,7 +56,7 @@ __device__ __forceinline__ const Seg& segment_of(const Args& p, int n) {
 struct I8Op {
     using Args = I8Args;
     static constexpr int BK = BK8;
-    static constexpr bool kAfterQuantize = true;
+    static constexpr bool kOverlapped = true;
     static __host__ __device__ constexpr uint32_t idesc(int M, int N) { return idesc_i8(M, N); }
     static __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
         mma_i8_pair_w(d, a, b, id, acc);
@@ -163,31 +164,27 @@ struct RowsShape {
     static constexpr int STAGES = (200 * 1024) / STAGE;
     static constexpr int OFF_BAR = STAGES * STAGE;
     static constexpr int N_BARS = 2 * STAGES + 5;   // full, empty, acc_full[2], acc_empty[2], drain
-    static constexpr int SMEM = OFF_BAR + N_BARS * 8 + 8 + 1024;
+    static constexpr int OFF_XS = (OFF_BAR + N_BARS * 8 + 8 + 15) & ~15;   // x_scale of the BT tokens
+    static constexpr int SMEM = OFF_XS + BT * 4 + 1024;
     static constexpr uint32_t TMEM_COLS = 2 * BT < 32 ? 32 : 2 * BT;
     static_assert(STAGE % 1024 == 0, "stage alignment");
     static_assert(SMEM <= 227 * 1024, "shared memory");
     static_assert(STAGES * STAGE >= BT * 128 * 4, "partial sums fit where the stages were");
 };
 
-// y[m][n] of one channel n, which dst / width place.
-__device__ __forceinline__ void store1(const I8Args& p, const Seg& sg, int64_t m, int n, int acc, float ws) {
-    const float y = (float)acc * (__ldg(p.x_scale + m) * ws);
-    const int64_t at = m * sg.width + (n - sg.n0);
-    if (p.out_f32) reinterpret_cast<float*>(sg.dst)[at] = y;
-    else sg.dst[at] = __float2bfloat16_rn(y);
-}
-
-__device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
-    int v;
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ int4 ld_cluster_int4(uint32_t addr) {
+    int4 v;
+    asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
     return v;
 }
 
-template <int BT>
+template <int BT, int kSplits>
 __global__ void __launch_bounds__(NT, 1)
 linear_i8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
-                      const __grid_constant__ I8Args p, int splits) {
+                      const __grid_constant__ I8Args p) {
     using S = RowsShape<BT>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
@@ -224,14 +221,15 @@ linear_i8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *s_tmem;
+    grid_dependency_trigger();
 
     // this CTA's k-blocks [k_lo, k_lo + kb_n) and tiles first, first + step, ...
-    const int rank = splits > 1 ? (int)cluster_rank() : 0;
+    const int rank = kSplits > 1 ? (int)cluster_rank() : 0;
     const int kb_all = (p.K + BK8 - 1) / BK8;
-    const int k_lo = (int)((int64_t)kb_all * rank / splits);
-    const int kb_n = (int)((int64_t)kb_all * (rank + 1) / splits) - k_lo;
+    const int k_lo = (int)((int64_t)kb_all * rank / kSplits);
+    const int kb_n = (int)((int64_t)kb_all * (rank + 1) / kSplits) - k_lo;
     const int tiles = p.n_blocks;
-    const int first = blockIdx.x / splits, step = gridDim.x / splits;
+    const int first = blockIdx.x / kSplits, step = gridDim.x / kSplits;
     const int my_tiles = first < tiles ? (tiles - first + step - 1) / step : 0;
 
     if (warp == 0) {
@@ -249,11 +247,12 @@ linear_i8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
                 const int kb = k_lo + (int)(it % kb_n);
                 tma_load_2d(sb + (uint32_t)s * S::STAGE + S::W_BYTES, &tm_x, kb * BK8, 0, full(s));
             };
+            if (!p.w_ready) grid_dependency_wait();
             for (uint32_t it = 0; it < pre; ++it) {
                 mbar_arrive_expect_tx(full(it), S::STAGE);
                 load_w(it, it);
             }
-            grid_dependency_wait();
+            if (p.w_ready) grid_dependency_wait();
             for (uint32_t it = 0; it < pre; ++it) load_x(it, it);
             bool ok = true;
             uint32_t it = pre;
@@ -319,31 +318,40 @@ linear_i8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
         const int q = warp & 3;
         const int row = q * 32 + lane;
         grid_dependency_wait();   // (the rows' scales)
+        float* xs = reinterpret_cast<float*>(smem + S::OFF_XS);
+        if ((int)threadIdx.x - 64 < BT) xs[threadIdx.x - 64] = (int)threadIdx.x - 64 < p.M ? p.x_scale[threadIdx.x - 64] : 0.0f;
+        asm volatile("bar.sync 1, 128;" ::: "memory");   // (the epilogue warps)
         bool ok = true;
         for (int ti = 0; ti < my_tiles; ++ti) {
             const uint32_t a = ti & 1u;
+            const int n = (first + ti * step) * 128 + row;
+            const float ws = n < p.N ? p.w_scale[n] : 0.0f;
+            const Seg& sg = segment_of(p, n);
             if (!mbar_wait_bounded(acc_full(a), (ti >> 1) & 1u) || *s_abort) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            const int n = (first + ti * step) * 128 + row;
             const uint32_t taddr = tmem + ((uint32_t)(q * 32) << 16) + a * BT;
-            const float ws = n < p.N ? p.w_scale[n] : 0.0f;
-            const Seg& sg = segment_of(p, n);
 #pragma unroll 1
             for (int c = 0; c < BT / 16; ++c) {
                 uint32_t r[16];
                 tmem_ld16(taddr + c * 16, r);
-                if (splits > 1) {   // [token][channel] int32 over the stages, all read by now
+                if constexpr (kSplits > 1) {   // [token][channel] int32 over the stages, all read by now
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         asm volatile("st.shared.b32 [%0], %1;" ::"r"(sb + ((c * 16 + i) * 128 + row) * 4), "r"(r[i])
                                      : "memory");
                 } else if (n < p.N) {
+                    const int64_t at = (int64_t)(c * 16) * sg.width + (n - sg.n0);
+                    const int left = (int)p.M - c * 16;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (c * 16 + i < p.M) store1(p, sg, c * 16 + i, n, (int)r[i], ws);
+                    for (int i = 0; i < 16; ++i) {
+                        if (i >= left) break;
+                        const float y = (float)(int)r[i] * (xs[c * 16 + i] * ws);
+                        if (p.out_f32) reinterpret_cast<float*>(sg.dst)[at + (int64_t)i * sg.width] = y;
+                        else sg.dst[at + (int64_t)i * sg.width] = __float2bfloat16_rn(y);
+                    }
                 }
             }
             tc_fence_before();
@@ -356,18 +364,37 @@ linear_i8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
         }
     }
 
-    if (splits > 1) {
-        // one tile per cluster: token m of it is added up by CTA m % splits
+    if constexpr (kSplits > 1) {
+        // One tile per cluster.  CTA m % kSplits adds up token m, a warp to a token and a
+        // lane to four channels.
         cluster_sync();
-        if (warp >= 2 && !*s_abort && my_tiles > 0) {
-            const int row = (warp & 3) * 32 + lane, n = first * 128 + row;
-            if (n < p.N) {
-                const Seg& sg = segment_of(p, n);
-                const float ws = p.w_scale[n];
-                for (int m = rank; m < p.M; m += splits) {
-                    int acc = 0;
-                    for (int r = 0; r < splits; ++r) acc += ld_cluster_s32(map_to_rank(sb + (m * 128 + row) * 4, r));
-                    store1(p, sg, m, n, acc, ws);
+        const int n = first * 128 + lane * 4;
+        if (warp >= 2 && !*s_abort && my_tiles > 0 && n < p.N) {
+            const float* xs = reinterpret_cast<const float*>(smem + S::OFF_XS);
+            const Seg& sg = segment_of(p, n);
+            const float4 ws = __ldg(reinterpret_cast<const float4*>(p.w_scale + n));
+#pragma unroll 2
+            for (int m = rank + (warp - 2) * kSplits; m < p.M; m += 4 * kSplits) {
+                int4 v[kSplits];
+#pragma unroll
+                for (int r = 0; r < kSplits; ++r) v[r] = ld_cluster_int4(map_to_rank(sb + (m * 128 + lane * 4) * 4, r));
+#pragma unroll
+                for (int r = 1; r < kSplits; ++r) {
+                    v[0].x += v[r].x;
+                    v[0].y += v[r].y;
+                    v[0].z += v[r].z;
+                    v[0].w += v[r].w;
+                }
+                const float f = xs[m];
+                const float4 y = make_float4((float)v[0].x * (f * ws.x), (float)v[0].y * (f * ws.y),
+                                             (float)v[0].z * (f * ws.z), (float)v[0].w * (f * ws.w));
+                const int64_t at = (int64_t)m * sg.width + (n - sg.n0);
+                if (p.out_f32) {
+                    *reinterpret_cast<float4*>(reinterpret_cast<float*>(sg.dst) + at) = y;
+                } else {
+                    *reinterpret_cast<uint2*>(sg.dst + at) =
+                        make_uint2(pack_bf16(__float_as_uint(y.x), __float_as_uint(y.y)),
+                                   pack_bf16(__float_as_uint(y.z), __float_as_uint(y.w)));
                 }
             }
         }

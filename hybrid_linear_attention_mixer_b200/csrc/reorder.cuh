@@ -34,6 +34,8 @@ struct Args {
 // Work item: NT * U vectors of one group's slots in one buffer.
 template <int WMAX, int U>
 __global__ void __launch_bounds__(NT) reorder_kernel(const __grid_constant__ Args p) {
+    grid_dependency_trigger();
+    grid_dependency_wait();
     for (int64_t it = blockIdx.x; it < p.total; it += gridDim.x) {
         const int64_t group = it / p.items;
         const int item = (int)(it % p.items);

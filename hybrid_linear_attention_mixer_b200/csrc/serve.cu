@@ -43,7 +43,11 @@ bool overlap(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; 
 bool float_dtype(int32_t d) { return d == GDN_BF16 || d == GDN_F32; }
 int elem(int32_t d) { return d == GDN_F32 ? 4 : d == GDN_BF16 ? 2 : 1; }
 
-// A launch that may start while the kernel before it on the stream still runs.
+// Every kernel here is launched so that it may start while the kernel before it on the
+// stream still runs (its set-up then costs no time of its own), and waits for that
+// kernel's end before it reads or writes any tensor; so whoever waits for one of them to
+// end has waited for all before it.  The one exception is a product's weights, behind
+// the rows that the same call makes 8-bit (I8Args::w_ready).
 struct Launch {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
@@ -53,13 +57,13 @@ struct Launch {
         cfg.dynamicSmemBytes = smem;
         cfg.stream = st;
         cfg.attrs = attr;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.numAttrs = 1;
     }
-    Launch& overlapped(bool on) {
-        if (on) {
-            attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-            attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
-        }
-        return *this;
+    template <typename... P, typename... A>
+    cudaError_t operator()(void (*kernel)(P...), const A&... args) {
+        return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
     }
     Launch& cluster(unsigned n) {
         if (n > 1) {
@@ -77,8 +81,7 @@ struct Launch {
 // ---------------------------------------------------------------------------
 template <typename TA, typename TR, bool kI8, int WARPS, int NV>
 cudaError_t launch_norm(const gdn::bnorm::Args& a, int64_t T, cudaStream_t st) {
-    gdn::bnorm::block_norm_kernel<TA, TR, kI8, WARPS, NV><<<(unsigned)T, WARPS * 32, 0, st>>>(a);
-    return cudaGetLastError();
+    return Launch((unsigned)T, WARPS * 32, 0, st)(gdn::bnorm::block_norm_kernel<TA, TR, kI8, WARPS, NV>, a);
 }
 
 template <typename TA, typename TR, bool kI8>
@@ -106,11 +109,10 @@ cudaError_t launch_quantize(const void* x, int64_t rows, int32_t cols, int8_t* q
     const T* xt = static_cast<const T*>(x);
     const unsigned grid = (unsigned)rows;
     const int nv = cols / 8;
-    if (nv <= 128) quantize_rows_kernel<T, 4, 1><<<grid, 128, 0, st>>>(xt, cols, q, scale);
-    else if (nv <= 384) quantize_rows_kernel<T, 4, 3><<<grid, 128, 0, st>>>(xt, cols, q, scale);
-    else if (nv <= 1024) quantize_rows_kernel<T, 8, 4><<<grid, 256, 0, st>>>(xt, cols, q, scale);
-    else quantize_rows_kernel<T, 16, 0><<<grid, 512, 0, st>>>(xt, cols, q, scale);
-    return cudaGetLastError();
+    if (nv <= 128) return Launch(grid, 128, 0, st)(quantize_rows_kernel<T, 4, 1>, xt, cols, q, scale);
+    if (nv <= 384) return Launch(grid, 128, 0, st)(quantize_rows_kernel<T, 4, 3>, xt, cols, q, scale);
+    if (nv <= 1024) return Launch(grid, 256, 0, st)(quantize_rows_kernel<T, 8, 4>, xt, cols, q, scale);
+    return Launch(grid, 512, 0, st)(quantize_rows_kernel<T, 16, 0>, xt, cols, q, scale);
 }
 
 gdn_status run_quantize(const void* x, int32_t x_dtype, int64_t rows, int32_t cols, int8_t* q, float* scale,
@@ -146,6 +148,7 @@ int resident_clusters(int size, unsigned threads, size_t smem) {
     if (cudaGetDevice(&dev) != cudaSuccess) return 1;
     if (dev < 64 && known[dev][slot]) return known[dev][slot];
     Launch l((unsigned)(sm_count() / size * size), threads, smem, nullptr);
+    l.cfg.numAttrs = 0;
     l.cluster((unsigned)size);
     if (size == 1) n = sm_count();
     else if (cudaOccupancyMaxActiveClusters(&n, Kernel, &l.cfg) != cudaSuccess || n <= 0) {
@@ -157,7 +160,7 @@ int resident_clusters(int size, unsigned threads, size_t smem) {
 }
 
 template <int BN>
-cudaError_t launch_i8_pair(const void* x, const void* w, gdn::gemm::I8Args a, bool behind_quantize, cudaStream_t st) {
+cudaError_t launch_i8_pair(const void* x, const void* w, gdn::gemm::I8Args a, cudaStream_t st) {
     using S = gdn::gemm::Shape2<BN>;
     using Op = gdn::gemm::I8Op;
     constexpr auto kernel = gdn::gemm::linear_pair_kernel<BN, Op>;
@@ -171,9 +174,7 @@ cudaError_t launch_i8_pair(const void* x, const void* w, gdn::gemm::I8Args a, bo
     cudaError_t e = allow_smem<kernel>(smem);
     if (e != cudaSuccess) return e;
     const int pairs = (int)std::min<int64_t>(a.tiles, resident_clusters<kernel>(2, threads, smem));
-    Launch l((unsigned)(2 * pairs), threads, smem, st);   // (the kernel names its cluster size)
-    l.overlapped(behind_quantize);
-    return cudaLaunchKernelEx(&l.cfg, kernel, tm_x, tm_w, a);
+    return Launch((unsigned)(2 * pairs), threads, smem, st)(kernel, tm_x, tm_w, a);   // (the kernel names its cluster size)
 }
 
 // Pair tile width for M > 128: as for bf16 (the operand bytes and the MMA time per
@@ -194,33 +195,44 @@ int pick_bn_i8(int64_t M, int N, int pairs) {
     return best;
 }
 
-template <int BT>
-cudaError_t launch_i8_rows(const void* x, const void* w, gdn::gemm::I8Args a, bool behind_quantize, cudaStream_t st) {
+template <int BT, int kSplits>
+struct RowsForm {
     using S = gdn::gemm::RowsShape<BT>;
-    constexpr auto kernel = gdn::gemm::linear_i8_rows_kernel<BT>;
+    static constexpr auto kernel = gdn::gemm::linear_i8_rows_kernel<BT, kSplits>;
+    static int at_once() { return resident_clusters<kernel>(kSplits, gdn::gemm::NT, S::SMEM); }
+    static cudaError_t launch(const CUtensorMap& tm_x, const CUtensorMap& tm_w, const gdn::gemm::I8Args& a,
+                              cudaStream_t st) {
+        const cudaError_t e = allow_smem<kernel>(S::SMEM);
+        if (e != cudaSuccess) return e;
+        const int grid = kSplits > 1 ? a.n_blocks * kSplits : std::min(a.n_blocks, sm_count());
+        return Launch((unsigned)grid, gdn::gemm::NT, S::SMEM, st).cluster(kSplits)(kernel, tm_x, tm_w, a);
+    }
+};
+
+template <int BT>
+cudaError_t launch_i8_rows(const void* x, const void* w, gdn::gemm::I8Args a, cudaStream_t st) {
     CUtensorMap tm_x, tm_w;
     if (!i8_map(&tm_x, x, a.M, a.K, BT) || !i8_map(&tm_w, w, a.N, a.K, 128)) return cudaErrorInvalidValue;
     a.n_blocks = (a.N + 127) / 128;
-    cudaError_t e = allow_smem<kernel>(S::SMEM);
-    if (e != cudaSuccess) return e;
-    // Split K where the tiles leave SMs idle: the k-blocks that the busiest CTA walks,
-    // and a few more for the join.
+    // Split K where the tiles leave SMs idle (one tile per cluster): the k-blocks that the
+    // busiest CTA walks, and a few more for the join.
     const int kb = (a.K + gdn::gemm::BK8 - 1) / gdn::gemm::BK8;
-    int splits = 1;
-    int64_t best = -1;
-    for (int s = 1; s <= 8 && s <= kb; s *= 2) {
-        const int at_once = resident_clusters<kernel>(s, gdn::gemm::NT, S::SMEM);
-        if (s > 1 && a.n_blocks > at_once) break;   // one tile per cluster
-        const int64_t cost = (int64_t)((a.n_blocks + at_once - 1) / at_once) * ((kb + s - 1) / s) + (s > 1 ? 4 : 0);
-        if (best < 0 || cost < best) {
-            best = cost;
-            splits = s;
+    const int at_once[4] = {sm_count(), RowsForm<BT, 2>::at_once(), RowsForm<BT, 4>::at_once(), RowsForm<BT, 8>::at_once()};
+    int best = 0;
+    int64_t best_cost = (int64_t)((a.n_blocks + at_once[0] - 1) / at_once[0]) * kb;
+    for (int i = 1; i < 4 && (1 << i) <= kb && a.n_blocks <= at_once[i]; ++i) {
+        const int64_t cost = (kb + (1 << i) - 1) / (1 << i) + 4;
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = i;
         }
     }
-    const int grid = splits > 1 ? a.n_blocks * splits : std::min(a.n_blocks, sm_count());
-    Launch l((unsigned)grid, gdn::gemm::NT, S::SMEM, st);
-    l.overlapped(behind_quantize).cluster((unsigned)splits);
-    return cudaLaunchKernelEx(&l.cfg, kernel, tm_x, tm_w, a, splits);
+    switch (best) {
+        case 0: return RowsForm<BT, 1>::launch(tm_x, tm_w, a, st);
+        case 1: return RowsForm<BT, 2>::launch(tm_x, tm_w, a, st);
+        case 2: return RowsForm<BT, 4>::launch(tm_x, tm_w, a, st);
+        default: return RowsForm<BT, 8>::launch(tm_x, tm_w, a, st);
+    }
 }
 
 // 8-bit rows, then their scales, in the workspace.
@@ -271,18 +283,19 @@ gdn_status run_linear_i8(const void* x, int32_t x_dtype, const float* x_scale, c
     }
     a.x_scale = x_scale;
     a.w_scale = w_scale;
+    a.w_ready = quantize;
     cudaError_t e;
-    if (M <= 16) e = launch_i8_rows<16>(x, w, a, quantize, st);
-    else if (M <= 32) e = launch_i8_rows<32>(x, w, a, quantize, st);
-    else if (M <= 64) e = launch_i8_rows<64>(x, w, a, quantize, st);
-    else if (M <= 128) e = launch_i8_rows<128>(x, w, a, quantize, st);
+    if (M <= 16) e = launch_i8_rows<16>(x, w, a, st);
+    else if (M <= 32) e = launch_i8_rows<32>(x, w, a, st);
+    else if (M <= 64) e = launch_i8_rows<64>(x, w, a, st);
+    else if (M <= 128) e = launch_i8_rows<128>(x, w, a, st);
     else {
         switch (pick_bn_i8(M, N, std::max(1, sm_count() / 2))) {
-            case 256: e = launch_i8_pair<256>(x, w, a, quantize, st); break;
-            case 224: e = launch_i8_pair<224>(x, w, a, quantize, st); break;
-            case 192: e = launch_i8_pair<192>(x, w, a, quantize, st); break;
-            case 160: e = launch_i8_pair<160>(x, w, a, quantize, st); break;
-            default: e = launch_i8_pair<128>(x, w, a, quantize, st); break;
+            case 256: e = launch_i8_pair<256>(x, w, a, st); break;
+            case 224: e = launch_i8_pair<224>(x, w, a, st); break;
+            case 192: e = launch_i8_pair<192>(x, w, a, st); break;
+            case 160: e = launch_i8_pair<160>(x, w, a, st); break;
+            default: e = launch_i8_pair<128>(x, w, a, st); break;
         }
     }
     return cuda_status(e);
@@ -351,8 +364,7 @@ cudaError_t launch_reorder(gdn::reorder::Args a, int64_t n_groups, cudaStream_t 
     a.items = items;
     a.total = (int64_t)items * n_groups;
     const unsigned grid = (unsigned)std::min<int64_t>(a.total, 0x7fffffff);
-    gdn::reorder::reorder_kernel<WMAX, U><<<grid, gdn::reorder::NT, 0, st>>>(a);
-    return cudaGetLastError();
+    return Launch(grid, gdn::reorder::NT, 0, st)(gdn::reorder::reorder_kernel<WMAX, U>, a);
 }
 
 }  // namespace
@@ -523,15 +535,13 @@ gdn_status gdn_beam_select(const void* logits, int32_t logits_dtype, int64_t ld,
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     a.total = (unsigned)(rows * L.slices);
     const unsigned grid = (a.total + gdn::beam::WARPS - 1) / gdn::beam::WARPS, block = 32 * gdn::beam::WARPS;
-    if (logits_dtype == GDN_BF16) gdn::beam::slice_kernel<__nv_bfloat16><<<grid, block, 0, st>>>(a);
-    else gdn::beam::slice_kernel<float><<<grid, block, 0, st>>>(a);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = logits_dtype == GDN_BF16 ? Launch(grid, block, 0, st)(gdn::beam::slice_kernel<__nv_bfloat16>, a)
+                                             : Launch(grid, block, 0, st)(gdn::beam::slice_kernel<float>, a);
     if (e != cudaSuccess) return cuda_status(e);
     e = allow_smem<gdn::beam::merge_kernel>(gdn::beam::kMaxMergeSmem);
     if (e != cudaSuccess) return cuda_status(e);
-    Launch l((unsigned)n_groups, gdn::beam::MT, gdn::beam::merge_smem(n_beams, L.slices, n_out), st);
-    l.overlapped(true);
-    return cuda_status(cudaLaunchKernelEx(&l.cfg, gdn::beam::merge_kernel, a));
+    return cuda_status(Launch((unsigned)n_groups, gdn::beam::MT, gdn::beam::merge_smem(n_beams, L.slices, n_out), st)(
+        gdn::beam::merge_kernel, a));
 }
 
 gdn_status gdn_reorder_states(const int32_t* parents, int32_t n_groups, int32_t n_beams,
