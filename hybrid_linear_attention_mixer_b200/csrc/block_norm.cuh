@@ -8,6 +8,11 @@
 // per bf16 element.  A row belongs to one block and stays in its registers through
 // the two or three reductions it needs (sum of o^2, sum of r^2, max |y|), which is
 // what keeps it to one pass; r passes to the second norm in fp32, unrounded.
+//
+// Two forms: for many rows a vector per thread (rows up to 2048) or 4 warps with a few, and
+// the weights read from L1 when they are used (4,095 rows of 1336: 15.8 us with 6 warps and
+// one vector, 17.5 with 4 warps and two); for few (fewer than the SMs hold at once, where a row's latency is
+// the call's) 16 warps a row and the weights fetched together with the row.
 #pragma once
 
 #include "device.cuh"
@@ -101,10 +106,22 @@ __device__ __forceinline__ float block_sum(float v, float* slot) {
     return v;
 }
 
+// 1 / (1 + exp(-g))
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+
+// Blocks an SM shall hold: 1024 threads of them where a thread's loads in flight (2 TA, 1 TR)
+// and its r leave that many registers; 47,200 rows of 2560 in bf16: 186 us, 194 with the 72
+// registers that the compiler takes by itself, 209 and 267 with 1280 and 1536 threads.
+template <typename TA, typename TR, int WARPS, int NV>
+constexpr int blocks_per_sm() {
+    return NV * (int)(4 * sizeof(TA) + 2 * sizeof(TR)) <= 36 && WARPS <= 8 ? 32 / WARPS : 1;
+}
+
 // One row per block of WARPS warps, NV vectors of 8 elements per thread.
 template <typename TA, typename TR, bool kI8, int WARPS, int NV>
-__global__ void __launch_bounds__(WARPS * 32) block_norm_kernel(const __grid_constant__ Args p) {
+__global__ void __launch_bounds__(WARPS * 32, blocks_per_sm<TA, TR, WARPS, NV>()) block_norm_kernel(const __grid_constant__ Args p) {
     constexpr int NT = WARPS * 32;
+    constexpr bool kFew = WARPS == 16 && NV <= 2;   // weights fetched with the row
     __shared__ float slot_o[WARPS], slot_r[WARPS];
     __shared__ uint32_t slot_y[WARPS];
     grid_dependency_trigger();
@@ -117,6 +134,7 @@ __global__ void __launch_bounds__(WARPS * 32) block_norm_kernel(const __grid_con
 
     Raw8<TR> xv[NV];
     Raw8<TA> ov[NV], gv[NV];
+    Raw8<float> post[kFew ? NV : 1], pre[kFew ? NV : 1];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int v = threadIdx.x + j * NT;
@@ -124,50 +142,60 @@ __global__ void __launch_bounds__(WARPS * 32) block_norm_kernel(const __grid_con
         if (o) ov[j].load(o + base + 8 * v);
         xv[j].load(x + base + 8 * v);
         if (p.gate_kind == GDN_GATE_FULL) gv[j].load(gate + base + 8 * v);
+        if constexpr (kFew) {
+            if (p.w_post) post[j].load(p.w_post + 8 * v);
+            if (p.w_pre) pre[j].load(p.w_pre + 8 * v);
+        }
     }
 
-    float f[NV][8];   // o, then r
     float inv_o = 1.0f;
-    if (o) {
+    if (p.w_post) {
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             if (threadIdx.x + j * NT >= nv) continue;
-            ov[j].get(f[j]);
+            float f[8];
+            ov[j].get(f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum = fmaf(f[j][i], f[j][i], sum);
+            for (int i = 0; i < 8; ++i) sum = fmaf(f[i], f[i], sum);
         }
-        if (p.w_post) inv_o = rsqrtf(block_sum<WARPS>(sum, slot_o) / (float)p.D + p.eps);
+        inv_o = rsqrtf(block_sum<WARPS>(sum, slot_o) / (float)p.D + p.eps);
     }
     float row_factor = p.res_scale * inv_o;
     if (p.gate_kind == GDN_GATE_TOKEN) {
         const float g = to_f32(gate[row]);
-        row_factor *= p.gate_sigmoid ? 1.0f / (1.0f + __expf(-g)) : g;
+        row_factor *= p.gate_sigmoid ? sigmoid(g) : g;
     }
 
+    float f[NV][8];   // r
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int v = threadIdx.x + j * NT;
         if (v >= nv) continue;
-        float xr[8];
-        xv[j].get(xr);
+        xv[j].get(f[j]);
         if (o) {
-            float g[8], w[8];
-            if (p.gate_kind == GDN_GATE_FULL) gv[j].get(g);
-            else if (p.gate_kind == GDN_GATE_CHANNEL) load8(static_cast<const float*>(p.gate) + 8 * v, g);
-            if (p.w_post) load8(p.w_post + 8 * v, w);
+            float n[8];
+            ov[j].get(n);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float n = f[j][i] * row_factor;
-                if (p.w_post) n *= w[i];
-                if (p.gate_kind >= GDN_GATE_CHANNEL) n *= p.gate_sigmoid ? 1.0f / (1.0f + __expf(-g[i])) : g[i];
-                f[j][i] = xr[i] + n;
+            for (int i = 0; i < 8; ++i) n[i] *= row_factor;
+            if (p.w_post) {
+                float w[8];
+                if constexpr (kFew) post[j].get(w);
+                else load8(p.w_post + 8 * v, w);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) n[i] *= w[i];
             }
-            store8(static_cast<TR*>(p.r) + base + 8 * v, f[j]);
-        } else {
+            if (p.gate_kind >= GDN_GATE_CHANNEL) {
+                float g[8];
+                if (p.gate_kind == GDN_GATE_FULL) gv[j].get(g);
+                else load8(static_cast<const float*>(p.gate) + 8 * v, g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[j][i] = xr[i];
+                for (int i = 0; i < 8; ++i) n[i] *= p.gate_sigmoid ? sigmoid(g[i]) : g[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[j][i] += n[i];
+            store8(static_cast<TR*>(p.r) + base + 8 * v, f[j]);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum = fmaf(f[j][i], f[j][i], sum);
@@ -181,7 +209,8 @@ __global__ void __launch_bounds__(WARPS * 32) block_norm_kernel(const __grid_con
         const int v = threadIdx.x + j * NT;
         if (v >= nv) continue;
         float w[8];
-        load8(p.w_pre + 8 * v, w);
+        if constexpr (kFew) pre[j].get(w);
+        else load8(p.w_pre + 8 * v, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[j][i] = f[j][i] * inv_r * w[i];
         if constexpr (kI8) m = quant::max_bits8(f[j], m);

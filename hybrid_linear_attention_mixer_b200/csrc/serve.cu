@@ -87,11 +87,18 @@ cudaError_t launch_norm(const gdn::bnorm::Args& a, int64_t T, cudaStream_t st) {
 template <typename TA, typename TR, bool kI8>
 cudaError_t norm_by_size(const gdn::bnorm::Args& a, int64_t T, cudaStream_t st) {
     const int nv = a.D / 8;
-    if (nv <= 128) return launch_norm<TA, TR, kI8, 4, 1>(a, T, st);
-    if (nv <= 256) return launch_norm<TA, TR, kI8, 4, 2>(a, T, st);
-    if (nv <= 384) return launch_norm<TA, TR, kI8, 4, 3>(a, T, st);
-    if (nv <= 512) return launch_norm<TA, TR, kI8, 4, 4>(a, T, st);
-    if (nv <= 1024) return launch_norm<TA, TR, kI8, 16, 2>(a, T, st);
+    if (T <= 2 * sm_count()) {   // few rows: the lowest latency
+        if (nv <= 512) return launch_norm<TA, TR, kI8, 16, 1>(a, T, st);
+        if (nv <= 1024) return launch_norm<TA, TR, kI8, 16, 2>(a, T, st);
+    } else {
+        if (nv <= 64) return launch_norm<TA, TR, kI8, 2, 1>(a, T, st);
+        if (nv <= 128) return launch_norm<TA, TR, kI8, 4, 1>(a, T, st);
+        if (nv <= 192) return launch_norm<TA, TR, kI8, 6, 1>(a, T, st);
+        if (nv <= 256) return launch_norm<TA, TR, kI8, 8, 1>(a, T, st);
+        if (nv <= 384) return launch_norm<TA, TR, kI8, 4, 3>(a, T, st);
+        if (nv <= 512) return launch_norm<TA, TR, kI8, 4, 4>(a, T, st);
+        if (nv <= 1024) return launch_norm<TA, TR, kI8, 8, 4>(a, T, st);
+    }
     return launch_norm<TA, TR, kI8, 16, 4>(a, T, st);
 }
 
