@@ -311,10 +311,13 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) slice_kernel(const __g
     auto vec = [&](int j) { return load_vec<T>(x, first + j * kStep, p.V, shift); };
     auto load_tile = [&](uint4 (&u)[VPT], int t) {
         if (t >= tiles) return;
+        const T* at = x + first + t * kTile;
         if (shift == 0 && begin + (t + 1) * kTile <= p.V) {
-            const T* at = x + first + t * kTile;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) u[j] = ld_once(at + j * kStep);
+        } else if (shift != 0 && begin + t * kTile > 0 && begin + (t + 1) * kTile + N <= p.V) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) u[j] = ld_shifted(reinterpret_cast<const uint8_t*>(at + j * kStep) - shift, shift);
         } else {
 #pragma unroll 1
             for (int j = 0; j < VPT; ++j) {
@@ -463,9 +466,11 @@ __device__ __forceinline__ double from_ordered64(uint64_t k) {
 }
 
 // One candidate of a group; better() is the order of the results.
+constexpr int kTokenBits = 20;
+static_assert(GDN_BEAM_MAX_VOCAB <= 1 << kTokenBits && kMaxBeams <= 1 << (32 - kTokenBits), "Cand::at");
 struct Cand {
     uint64_t score;   // ordered; 0: none
-    uint32_t at;      // w * V + v
+    uint32_t at;      // w * 2^20 + v: in the order of w * V + v
     uint32_t rough;   // the score rounded down to fp32, ordered; 0: none
 };
 __device__ __forceinline__ bool better(const Cand& a, const Cand& b) {
@@ -545,7 +550,7 @@ constexpr size_t kMaxKeyBytes = 64 * 1024;
 constexpr int kFew = 96;               // candidates that are ranked as they are
 constexpr int kMaxLists = 4096;        // of a group
 constexpr size_t kMaxMergeSmem = (kMaxLists + (size_t)kMaxOut * kMaxOut) * sizeof(Cand) + kMaxKeyBytes;
-static_assert(kMaxMergeSmem <= 225 * 1024, "shared memory of the merge");
+static_assert(kMaxMergeSmem <= 210 * 1024, "shared memory of the merge");
 __host__ __device__ constexpr int merge_cap(int n) { return n * n < 512 ? 512 : n * n; }   // candidates
 inline size_t merge_key_bytes(int W, int slices, int n) { return (size_t)W * slices * n * sizeof(uint64_t); }
 inline size_t merge_smem(int W, int slices, int n) {
@@ -562,13 +567,14 @@ __global__ void __launch_bounds__(MT) merge_kernel(const __grid_constant__ Args 
     __shared__ double ref[kMaxBeams], offset[kMaxBeams];
     __shared__ uint8_t kind[kMaxBeams];    // 0: no candidates, 1: from the logits, 2: finished
     __shared__ int sel[kMaxOut];           // the lists of the n best heads, best first
-    __shared__ int s_n, s_few;
+    __shared__ int s_n, s_few, s_lists;
+    __shared__ uint16_t s_list[kMaxLists]; // the lists whose heads reach the bound
     __shared__ Scratch scratch[2];
     __shared__ Cand few[kFew];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row0 = (int64_t)blockIdx.x * p.W;
     const int lists = p.W * p.slices;
-    if (tid == 0) s_n = s_few = 0;
+    if (tid == 0) s_n = s_few = s_lists = 0;
     grid_dependency_trigger();
     grid_dependency_wait();
     const uint64_t* keys = p.cand + row0 * p.slices * p.n;
@@ -580,15 +586,18 @@ __global__ void __launch_bounds__(MT) merge_kernel(const __grid_constant__ Args 
 
     for (int w = warp; w < p.W; w += MT / 32) {
         const int64_t row = row0 + w;
+        const Stat* st = p.stats + row * p.slices;
+        Stat mine = lane < p.slices ? st[lane] : Stat{0.0, -INFINITY, -INFINITY};   // (used only if the row is live)
         const float score = p.scores[row];
         const bool fin = p.finished && p.finished[row];
         double off = score;
         float top = -INFINITY;
         if (!fin && isfinite(score)) {
-            const Stat* st = p.stats + row * p.slices;
-            float c = -INFINITY;
-            bool fast = true;
-            for (int s = lane; s < p.slices; s += 32) {
+            // sums of exp(x) / (2^c exp(-top kScale)), or, some c being NaN, / exp(top)
+            float c = mine.c;
+            top = mine.top;
+            bool fast = !isnan(mine.c);
+            for (int s = lane + 32; s < p.slices; s += 32) {
                 top = fmaxf(top, st[s].top);
                 c = fmaxf(c, st[s].c);
                 fast &= !isnan(st[s].c);
@@ -599,15 +608,17 @@ __global__ void __launch_bounds__(MT) merge_kernel(const __grid_constant__ Args 
                 c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, d));
             }
             fast = __all_sync(0xffffffffu, fast);
-            double sum = 0.0;   // of exp(x) / (2^c exp(-top kScale)), or / exp(top)
-            for (int s = lane; s < p.slices; s += 32) {
-                const Stat t = st[s];
-                double f = 0.0;   // (no logits: t.sum is 0, or the NaN that has to show)
-                if (!(t.top > -INFINITY)) f = 1.0;
-                else if (fast)   // (exp of a number below 2e-3, and of 1e-6 where it matters)
-                    f = pow2(t.c - c) * (1.0 - ((double)t.top - (double)top) * kScale);
-                else f = exp((isnan(t.c) ? (double)t.top : (double)t.c * kLn2 - (double)t.top * kScale) - (double)top);
-                sum += t.sum * f;
+            double sum = 0.0;
+            for (int s = lane;;) {
+                // (no logits: the sum is 0, or the NaN that has to show)
+                double f = 1.0;
+                if (mine.top > -INFINITY)
+                    f = fast ? pow2(mine.c - c) * (1.0 - ((double)mine.top - (double)top) * kScale)   // (exp of 1e-6 at most where it matters)
+                             : exp((isnan(mine.c) ? (double)mine.top : (double)mine.c * kLn2 - (double)mine.top * kScale) -
+                                   (double)top);
+                sum += mine.sum * f;
+                if ((s += 32) >= p.slices) break;
+                mine = st[s];
             }
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -622,38 +633,44 @@ __global__ void __launch_bounds__(MT) merge_kernel(const __grid_constant__ Args 
         }
     }
     __syncthreads();
-    // Entry e of list l: beam l / slices, slice l % slices.  A finished beam's one entry is
-    // the first of its first list.
-    auto entry = [&](int l, int e) {
-        const int w = l / p.slices;
+    // Entry e of list l, which is beam w's.  A finished beam's one entry is the first of its
+    // first list.
+    auto entry = [&](int l, int w, int e) {
         double score = offset[w];
-        Cand c{0, (uint32_t)w * p.V + p.pad, 0};
+        Cand c{0, (uint32_t)(w << kTokenBits | p.pad), 0};
         if (kind[w] == 1) {
             const uint64_t k = keys[l * p.n + e];
             if (!k) return c;
             score += (double)from_ordered((uint32_t)(k >> 32)) - ref[w];
-            c.at = (uint32_t)w * p.V + (0xffffffffu - (uint32_t)k);
-        } else if (kind[w] == 0 || l % p.slices != 0 || e != 0) {
+            c.at = (uint32_t)w << kTokenBits | (0xffffffffu - (uint32_t)k);
+        } else if (kind[w] == 0 || l != w * p.slices || e != 0) {
             return c;
         }
         c.score = ordered64(score);
         c.rough = ordered(__double2float_rd(score));
         return c;
     };
-    // What n heads reach, the n best candidates reach: they are collected, a warp to a list,
-    // and narrowed down once more, since one beam's may be most of them.
-    for (int l = tid; l < lists; l += MT) head[l] = entry(l, 0);
+    // What n heads reach, the n best candidates reach: they are collected, and narrowed down
+    // once more, since one beam's may be most of them.
+    for (int l = tid; l < lists; l += MT) head[l] = entry(l, l / p.slices, 0);
     __syncthreads();
     const uint32_t bound = block_bound(head, lists, p.n, &scratch[0]);
-    for (int l = warp; l < lists; l += MT / 32) {
-        if (head[l].rough < bound) continue;
-        for (int e = lane; e < p.n; e += 32) {
-            const Cand c = entry(l, e);
-            if (c.rough >= bound) {
-                const int k = atomicAdd(&s_n, 1);
-                if (k < merge_cap(p.n)) cand[k] = c;
-            }
+    auto collect = [&](const Cand& c) {
+        const int k = atomicAdd(&s_n, 1);
+        if (k < merge_cap(p.n)) cand[k] = c;
+    };
+    for (int l = tid; l < lists; l += MT)
+        if (head[l].rough >= bound) {
+            collect(head[l]);
+            s_list[atomicAdd(&s_lists, 1)] = (uint16_t)l;
         }
+    __syncthreads();
+    const int bits = 32 - __clz(p.n - 1);   // n <= 2^bits
+    for (int i = tid; i < s_lists << bits; i += MT) {
+        const int l = s_list[i >> bits], e = i & ((1 << bits) - 1);
+        if (e == 0 || e >= p.n) continue;
+        const Cand c = entry(l, head[l].at >> kTokenBits, e);
+        if (c.rough >= bound) collect(c);
     }
     __syncthreads();
     if (s_n > merge_cap(p.n)) {
@@ -667,7 +684,8 @@ __global__ void __launch_bounds__(MT) merge_kernel(const __grid_constant__ Args 
         const Cand last = head[sel[p.n - 1]];
         __syncthreads();
         for (int i = tid; i < p.n * p.n; i += MT) {
-            const Cand c = entry(sel[i / p.n], i % p.n);
+            const int l = sel[i / p.n];
+            const Cand c = entry(l, head[l].at >> kTokenBits, i % p.n);
             if (c.score && !better(last, c)) cand[atomicAdd(&s_n, 1)] = c;
         }
         __syncthreads();
@@ -690,8 +708,8 @@ __global__ void __launch_bounds__(MT) merge_kernel(const __grid_constant__ Args 
     const int64_t out = (int64_t)blockIdx.x * p.n;
     rank_all(from, total, [&](int i, int rank) {
         if (rank >= p.n) return;
-        p.parents[out + rank] = (int32_t)(from[i].at / (uint32_t)p.V);
-        p.tokens[out + rank] = (int32_t)(from[i].at % (uint32_t)p.V);
+        p.parents[out + rank] = (int32_t)(from[i].at >> kTokenBits);
+        p.tokens[out + rank] = (int32_t)(from[i].at & ((1u << kTokenBits) - 1u));
         p.out_scores[out + rank] = (float)from_ordered64(from[i].score);
     });
     for (int i = total + tid; i < p.n; i += MT) {

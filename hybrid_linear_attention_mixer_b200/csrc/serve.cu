@@ -311,7 +311,7 @@ gdn_status run_linear_i8(const void* x, int32_t x_dtype, const float* x_scale, c
 // ---------------------------------------------------------------------------
 // Beam selection
 // ---------------------------------------------------------------------------
-constexpr int kBeamTiles = 4;
+constexpr int kBeamTiles = 2;
 constexpr int kBeamWarps = 148 * 32;    // the slice warps that the GPU holds
 
 struct BeamLayout {
