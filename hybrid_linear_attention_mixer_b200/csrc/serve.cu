@@ -41,7 +41,7 @@ Span span(const void* p, int64_t bytes) {
 bool overlap(const Span& a, const Span& b) { return a.lo < b.hi && b.lo < a.hi; }
 
 bool float_dtype(int32_t d) { return d == GDN_BF16 || d == GDN_F32; }
-int elem(int32_t d) { return d == GDN_F32 ? 4 : d == GDN_BF16 ? 2 : 1; }
+int64_t elem(int32_t d) { return d == GDN_F32 ? 4 : d == GDN_BF16 ? 2 : 1; }
 
 // Every kernel here is launched so that it may start while the kernel before it on the
 // stream still runs (its set-up then costs no time of its own), and waits for that
@@ -276,9 +276,21 @@ gdn_status run_linear_i8(const void* x, int32_t x_dtype, const float* x_scale, c
         return GDN_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool quantize = x_dtype != GDN_I8;
+    const size_t ws_need = quantize ? gdn_linear_i8_workspace_size(M, K) : 0;
+    // what is written (the workspace last), what is read
+    Span outs[GDN_LINEAR_MAX_SEGMENTS + 1];
+    for (int i = 0; i < n_segs; ++i) outs[i] = span(segs[i].dst, M * segs[i].width * elem(out_dtype));
+    outs[n_segs] = quantize ? span(workspace, (int64_t)ws_need) : Span{0, 0};
+    const Span ins[4] = {span(x, M * K * elem(x_dtype)), span(x_scale, M * 4), span(w, (int64_t)N * K), span(w_scale, (int64_t)N * 4)};
+    for (int i = 0; i <= n_segs; ++i) {
+        for (int j = i + 1; j <= n_segs; ++j)
+            if (overlap(outs[i], outs[j])) return GDN_ERR_INVALID_ARG;
+        for (const Span& in : ins)
+            if (overlap(outs[i], in)) return GDN_ERR_INVALID_ARG;
+    }
     if (quantize) {
         if (x_scale || !workspace || !aligned(workspace, 256)) return GDN_ERR_INVALID_ARG;
-        if (workspace_bytes < gdn_linear_i8_workspace_size(M, K)) return GDN_ERR_WORKSPACE;
+        if (workspace_bytes < ws_need) return GDN_ERR_WORKSPACE;
         int8_t* q = static_cast<int8_t*>(workspace);
         float* scale = reinterpret_cast<float*>(q + i8_scale_off(M, K));
         const gdn_status s = run_quantize(x, x_dtype, M, K, q, scale, st);
@@ -578,9 +590,10 @@ gdn_status gdn_reorder_states(const int32_t* parents, int32_t n_groups, int32_t 
     }
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (n_beams <= 4) e = launch_reorder<4, 4>(a, n_groups, st);
+    if (n_beams <= 2) e = launch_reorder<2, 8>(a, n_groups, st);
+    else if (n_beams <= 4) e = launch_reorder<4, 4>(a, n_groups, st);
     else if (n_beams <= 8) e = launch_reorder<8, 2>(a, n_groups, st);
-    else if (n_beams <= 16) e = launch_reorder<16, 1>(a, n_groups, st);
+    else if (n_beams <= 16) e = launch_reorder<16, 2>(a, n_groups, st);
     else e = launch_reorder<32, 1>(a, n_groups, st);
     return cuda_status(e);
 }

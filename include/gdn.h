@@ -363,8 +363,8 @@ void gdn_norm_config_default(gdn_norm_config* cfg);
  *      y NULL (then w_pre and y_scale must be NULL): only the residual sum
  * r may be x, and y (not in int8) may be o; no other two tensors may overlap.
  * Tensors are 16-byte aligned (y_scale and a token gate: to their element).
- * T == 0 is a no-op.  A row whose mean square is beyond fp32 (entries above about
- * 1e19) has the norm 0; one with an infinity or a NaN gives NaN.
+ * T == 0 is a no-op.  A row whose sum of squares is beyond fp32 (entries above about
+ * 1e19 / sqrt(dim)) has the norm 0; one with an infinity or a NaN gives NaN.
  */
 gdn_status gdn_block_norm(const gdn_norm_config* cfg, const void* o, const void* x, const void* gate,
                           const float* w_post, const float* w_pre, int64_t T, void* r, void* y,
@@ -396,8 +396,9 @@ gdn_status gdn_quantize_rows(const void* x, int32_t x_dtype, int64_t rows, int32
  *   K a multiple of 16, at most 131056 (128 * 128 * K must fit in 31 bits); N a
  *   multiple of 8 (else GDN_ERR_UNSUPPORTED).  The columns of y are split over segs
  *   as in gdn_linear; dst holds out_dtype (GDN_BF16 or GDN_F32).
- * x, w and the destinations are 16-byte aligned.  The scales may be anything,
- * NaN and infinities included.  M == 0 is a no-op.
+ * x, w, w_scale and the destinations are 16-byte aligned.  The scales may be
+ * anything, NaN and infinities included.  Nothing written (the destinations, the
+ * workspace) may overlap anything else.  M == 0 is a no-op.
  */
 size_t gdn_linear_i8_workspace_size(int64_t M, int32_t K);
 gdn_status gdn_linear_i8(const void* x, int32_t x_dtype, const float* x_scale, const int8_t* w,

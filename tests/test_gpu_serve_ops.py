@@ -285,6 +285,19 @@ def test_linear_i8_many_rows_offsets_past_32_bits():
     check_linear(y, x, xs, w, ws, "bf16", rows=slice(0, 40))
 
 
+@pytest.mark.parametrize("M", [3, 40, 100, 200])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_linear_i8_writes_its_rows_only(M, out):
+    """What lies behind the last row stays as it was (tiles reach past it)."""
+    N, K = 392, 272
+    x, xs, w, ws = i8_case(M, N, K, M, "i8")
+    widths = (136, 256)
+    big = [torch.full((M + 130, wd), 7.0, dtype=DT[out], device=DEV) for wd in widths]
+    gdn.linear_i8(x, w, ws, x_scale=xs, outs=[b[:M] for b in big])
+    check_linear(torch.cat([b[:M] for b in big], 1), x, xs, w, ws, out)
+    assert all((b[M:] == 7.0).all() for b in big)
+
+
 def test_projections_i8():
     cfg = gdn.Config()
     for T in (1, 70, 150):
@@ -623,6 +636,83 @@ def test_decode_step_replays_from_a_graph():
         assert all(torch.equal(s.got[n], ref[n]) for n in ("o", "y", "f", "lg", "par", "tok", "sc"))
         assert torch.equal(s.conv, ref["conv"]) and torch.equal(s.rec, ref["rec"]) and torch.equal(s.x_run, ref["x"])
     del graph
+
+
+def test_graphs_that_share_a_workspace():
+    """Two captured steps of different sizes over one set of workspaces, replayed in turn."""
+    steps = [Step(2, 2, 4096, 25), Step(1, 3, 8192, 26)]
+    size = {n: max(s.ws[n].numel() for s in steps) for n in steps[0].ws}
+    shared = {n: torch.empty(v, dtype=torch.uint8, device=DEV) for n, v in size.items()}
+    ref, graphs = [], []
+    for s in steps:
+        s.ws = shared
+        s.run()
+        torch.cuda.synchronize()
+        ref.append((s.scores.clone(), s.rec.clone(), s.x_run.clone()))
+        g, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st), torch.cuda.graph(g, stream=st):
+            s.run()
+        graphs.append(g)
+    for _ in range(3):
+        for s in steps:
+            s.reset()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        gdn.check_device_error()
+        for s, r in zip(steps, ref):
+            assert torch.equal(s.scores, r[0]) and torch.equal(s.rec, r[1]) and torch.equal(s.x_run, r[2])
+    del graphs
+
+
+FIRST_CALL = """
+import sys
+sys.path[:0] = [%r, %r]
+import torch
+import test_gpu_serve_ops as T
+s = T.Step(1, 2, 4096, 27)   # (its weights' 8-bit rows are the library's first call)
+torch.cuda.synchronize()
+g, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+st.wait_stream(torch.cuda.current_stream())
+with torch.cuda.stream(st), torch.cuda.graph(g, stream=st):
+    s.run()
+g.replay()
+torch.cuda.synchronize()
+T.gdn.check_device_error()
+got = (s.scores.clone(), s.rec.clone(), s.x_run.clone())
+s.reset()
+s.run()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, (s.scores, s.rec, s.x_run)))
+print("captured first")
+"""
+
+
+def test_first_calls_may_be_captured():
+    """A process that captures the products, the selection and the reordering before it has
+    ever made such a call directly."""
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALL % (os.path.dirname(here), here)], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "captured first" in r.stdout, r.stdout + r.stderr
+
+
+def test_reorder_after_selection_of_a_whole_model():
+    """The states of 36 layers in one call (72 buffers)."""
+    G, W, Lr = 1, 4, 36
+    rec = torch.randn((Lr, G * W, 6, 32, 32), device=DEV)
+    conv = torch.randn((Lr, G * W, 320, 3), device=DEV).to(torch.bfloat16)
+    before = rec.clone(), conv.clone()
+    logits, scores = beam_case(G, W, 20000, "bf16", 28)
+    par, _, _ = gdn.beam_select(logits, scores)
+    gdn.reorder_states(par, gdn.reorder_plan(list(rec) + list(conv), G, W))
+    gdn.check_device_error()
+    at = par[0].long()
+    assert torch.equal(rec, before[0][:, at]) and torch.equal(conv, before[1][:, at])
 
 
 def test_two_streams_at_once():

@@ -121,6 +121,12 @@ def test_linear_i8_argument_errors(lib):
     assert call(dt=BF16, xs=0, wk=0, wkb=size) == INVALID
     assert call(dt=BF16, xs=0, wk=8 * MB + 16, wkb=size) == INVALID
     assert call(dt=F32, xs=0, wk=8 * MB, wkb=size - 1) == WORKSPACE
+    # nothing written may overlap anything else
+    for ptr in (MB, MB + 128, 2 * MB, 3 * MB + 64 * 64 - 16, 4 * MB):
+        assert call(sg=_segs(64, ptr=ptr)) == INVALID
+    assert call(N=128, sg=_segs(64, 64)) == INVALID                            # one destination twice
+    for wk in (MB, 3 * MB, 4 * MB, 64 * MB):
+        assert call(dt=BF16, xs=0, wk=wk, wkb=size) == INVALID
 
 
 def test_projections_i8_argument_errors(lib):
