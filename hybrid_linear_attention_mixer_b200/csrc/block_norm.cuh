@@ -36,46 +36,6 @@ struct Args {
     float eps, res_scale;
 };
 
-// 16-byte loads that do not displace the weights from L1 (each row is read once).
-__device__ __forceinline__ uint4 ld_stream(const void* p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p)
-                 : "memory");
-    return v;
-}
-
-// Eight consecutive values of a row, kept as loaded.
-template <typename T>
-struct Raw8;
-template <>
-struct Raw8<__nv_bfloat16> {
-    uint4 u;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = ld_stream(p); }
-    __device__ __forceinline__ void get(float (&f)[8]) const {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-    }
-};
-template <>
-struct Raw8<float> {
-    uint4 a, b;
-    __device__ __forceinline__ void load(const float* p) {
-        a = ld_stream(p);
-        b = ld_stream(p + 4);
-    }
-    __device__ __forceinline__ void get(float (&f)[8]) const {
-        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
-    }
-};
-
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&f)[8]) {
     uint32_t w[4];
 #pragma unroll
@@ -132,6 +92,7 @@ __global__ void __launch_bounds__(WARPS * 32, blocks_per_sm<TA, TR, WARPS, NV>()
     const TR* x = static_cast<const TR*>(p.x);
     const TA* gate = static_cast<const TA*>(p.gate);
 
+    using quant::Raw8;
     Raw8<TR> xv[NV];
     Raw8<TA> ov[NV], gv[NV];
     Raw8<float> post[kFew ? NV : 1], pre[kFew ? NV : 1];

@@ -20,6 +20,57 @@ namespace quant {
 
 constexpr uint32_t kInfBits = 0x7f800000u;
 
+// 16-byte loads of what is read once: they leave L1 to what is not.
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
+// Eight consecutive values of a row, kept as loaded.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<__nv_bfloat16> {
+    uint4 u;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = ld_stream(p); }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    // the largest |x|, as its fp32 bit pattern (which orders finite < infinity < NaN)
+    __device__ __forceinline__ uint32_t max_bits() const {
+        constexpr uint32_t kAbs = 0x7fff7fffu;
+        const uint32_t m = __vmaxu2(__vmaxu2(u.x & kAbs, u.y & kAbs), __vmaxu2(u.z & kAbs, u.w & kAbs));
+        return max(m << 16, m & 0xffff0000u);
+    }
+};
+template <>
+struct Raw8<float> {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = ld_stream(p);
+        b = ld_stream(p + 4);
+    }
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(w[i]);
+    }
+    __device__ __forceinline__ uint32_t max_bits() const {
+        constexpr uint32_t kAbs = 0x7fffffffu;
+        return max(max(max(a.x & kAbs, a.y & kAbs), max(a.z & kAbs, a.w & kAbs)),
+                   max(max(b.x & kAbs, b.y & kAbs), max(b.z & kAbs, b.w & kAbs)));
+    }
+};
+
 // What a row's elements are divided by.  The largest |x| comes as its bit pattern,
 // which orders finite < infinity < NaN.
 struct RowScale {
@@ -48,11 +99,17 @@ __device__ __forceinline__ uint2 pack_i8(const float (&f)[8], const RowScale& s)
     constexpr float kNear = 0.5f - 0x1p-12f;   // |t| <= 127, so t is off by 2^-14 at most
     uint32_t q[8];
     float off = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float t = (f[i] * s.c) * s.inv, r = t + kRound;
+    auto round = [&](int i, float t) {
+        const float r = t + kRound;
         off = fmaxf(off, fabsf(t - (r - kRound)));
         q[i] = __float_as_uint(r);
+    };
+    if (s.c == 1.0f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) round(i, f[i] * s.inv);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) round(i, (f[i] * s.c) * s.inv);
     }
     if (off > kNear) {
 #pragma unroll
@@ -100,33 +157,38 @@ quantize_rows_kernel(const T* __restrict__ x, int cols, int8_t* __restrict__ q, 
     const int nv = cols / 8;
     uint32_t m = 0;
     if constexpr (NV > 0) {
-        float f[NV][8];
+        Raw8<T> v[NV];
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int v = threadIdx.x + j * NT;
-            if (v < nv) {
-                load8(xr + 8 * v, f[j]);
-                m = max_bits8(f[j], m);
-            }
+            const int i = threadIdx.x + j * NT;
+            if (i < nv) v[j].load(xr + 8 * i);
         }
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (threadIdx.x + j * NT < nv) m = max(m, v[j].max_bits());
         const RowScale s = row_scale(block_max<WARPS>(m, slot));
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int v = threadIdx.x + j * NT;
-            if (v < nv) *reinterpret_cast<uint2*>(qr + 8 * v) = pack_i8(f[j], s);
+            const int i = threadIdx.x + j * NT;
+            if (i >= nv) continue;
+            float f[8];
+            v[j].get(f);
+            *reinterpret_cast<uint2*>(qr + 8 * i) = pack_i8(f, s);
         }
         if (threadIdx.x == 0) scale[row] = s.scale;
     } else {
-        for (int v = threadIdx.x; v < nv; v += NT) {
-            float f[8];
-            load8(xr + 8 * v, f);
-            m = max_bits8(f, m);
+        for (int i = threadIdx.x; i < nv; i += NT) {
+            Raw8<T> v;
+            v.load(xr + 8 * i);
+            m = max(m, v.max_bits());
         }
         const RowScale s = row_scale(block_max<WARPS>(m, slot));
-        for (int v = threadIdx.x; v < nv; v += NT) {
+        for (int i = threadIdx.x; i < nv; i += NT) {
+            Raw8<T> v;
             float f[8];
-            load8(xr + 8 * v, f);
-            *reinterpret_cast<uint2*>(qr + 8 * v) = pack_i8(f, s);
+            v.load(xr + 8 * i);
+            v.get(f);
+            *reinterpret_cast<uint2*>(qr + 8 * i) = pack_i8(f, s);
         }
         if (threadIdx.x == 0) scale[row] = s.scale;
     }
