@@ -190,7 +190,9 @@ __device__ __forceinline__ uint4 ld_shifted(const uint8_t* p, int shift) {
 
 // A row is live when it can give candidates from its logits.
 __device__ __forceinline__ bool row_live(const Args& p, int64_t row) {
-    return !(p.finished && p.finished[row]) && isfinite(p.scores[row]);
+    const float score = p.scores[row];   // (both on their way at once)
+    const uint8_t ended = p.finished ? p.finished[row] : 0;
+    return !ended && isfinite(score);
 }
 
 // Elements [i0, i0 + N) of a row that starts `shift` bytes into a 16-byte vector; -inf

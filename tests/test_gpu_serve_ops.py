@@ -666,6 +666,60 @@ def test_graphs_that_share_a_workspace():
     del graphs
 
 
+def test_prefill_between_8_bit_projections():
+    """hidden -> norm to 8 bits -> in_proj -> prefill, whose work forks onto side streams ->
+    out_proj -> norm with the residual, queued at once and from a graph: what the same calls
+    give with a synchronisation after each."""
+    T, cfg = 4200, gdn.Config(prefill_segments=3)
+    g = torch.Generator(device=DEV).manual_seed(29)
+    rnd = lambda *s, dt=torch.bfloat16, k=1.0: (torch.randn(s, generator=g, device=DEV) * k).to(dt)
+    w = {"conv_w": rnd(10240, 4, dt=torch.float32, k=0.5), "A_log": torch.rand(48, generator=g, device=DEV),
+         "dt_bias": rnd(48, dt=torch.float32, k=0.1), "norm_w": torch.ones(128, device=DEV)}
+    n1, n2, n3 = (1 + rnd(2560, dt=torch.float32, k=0.1) for _ in range(3))
+    w_in, w_out = (gdn.quantize_rows(rnd(n, k, k=k ** -0.5)) for n, k in ((16480, 2560), (2560, 6144)))
+    x, gate = rnd(T, 2560), rnd(T, 2560)
+    cu = torch.tensor([0, 1500, T], dtype=torch.int32, device=DEV)
+    conv, rec = torch.zeros((2, 10240, 3), dtype=torch.bfloat16, device=DEV), torch.zeros((2, 48, 128, 128), device=DEV)
+    ws = torch.empty(gdn.workspace_size(cfg, T, 2), dtype=torch.uint8, device=DEV)
+    ws8 = torch.empty(gdn.linear_i8_workspace_size(T, 6144), dtype=torch.uint8, device=DEV)
+    ncfg = gdn.NormConfig(gate="full", gate_act="sigmoid", res_scale=0.5)
+
+    def run(between=lambda: None):
+        conv.zero_()
+        rec.zero_()
+        out = []
+        _, h, hs = gdn.block_norm(gdn.NormConfig(), None, x, w_pre=n1, quantize=True)
+        between()
+        p = gdn.in_proj_i8(cfg, h, *w_in, hidden_scale=hs)
+        between()
+        o = gdn.prefill(cfg, w, p["q"], p["k"], p["v"], p["a"], p["b"], p["z"], conv, rec, cu, workspace=ws)
+        between()
+        y = gdn.out_proj_i8(cfg, o, *w_out, workspace=ws8)
+        between()
+        r, f, _ = gdn.block_norm(ncfg, y, x, gate, n2, n3)
+        between()
+        return [o, y, r, f]
+
+    ref = [t.clone() for t in run(torch.cuda.synchronize)] + [conv.clone(), rec.clone()]
+    gdn.check_device_error()
+    for _ in range(3):
+        got = run()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got + [conv, rec], ref))
+    graph, st = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st), torch.cuda.graph(graph, stream=st):
+        got = run()
+    for _ in range(2):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        gdn.check_device_error()
+        assert all(torch.equal(a, b) for a, b in zip(got + [conv, rec], ref))
+    del graph
+
+
 FIRST_CALL = """
 import sys
 sys.path[:0] = [%r, %r]
