@@ -188,8 +188,10 @@ cudaError_t launch_i8_pair(const void* x, const void* w, gdn::gemm::I8Args a, cu
     return Launch((unsigned)(2 * pairs), threads, smem, st)(kernel, tm_x, tm_w, a);   // (the kernel names its cluster size)
 }
 
-// Pair tile width for M > 128: as for bf16 (the operand bytes and the MMA time per
-// k-block are the same), over the widths that kind::i8 has at M = 256.
+// Pair tile width for M > 128, over the widths that kind::i8 has at M = 256: fewest
+// waves x (operand bytes of a k-block, 128 x (256 + BN) of a pair).  The bytes from L2 bound
+// a k-block, not the MMA, which takes half the bf16 form's time: 4096 x 16480 x 2560 at 256
+// (15 waves) 127 us, at 224 (16) 131, at 192 (19) 142; the bf16 form's rule took 224.
 int pick_bn_i8(int64_t M, int N, int pairs) {
     static const int cand[] = {256, 224, 192, 160, 128};
     const int64_t mp = (M + 2 * gdn::gemm::BM - 1) / (2 * gdn::gemm::BM);
@@ -197,7 +199,7 @@ int pick_bn_i8(int64_t M, int N, int pairs) {
     int64_t best_cost = -1;
     for (int bn : cand) {
         const int64_t tiles = mp * ((N + bn - 1) / bn);
-        const int64_t cost = (tiles + pairs - 1) / pairs * std::max<int64_t>(256 + bn, 17 * bn / 8);
+        const int64_t cost = (tiles + pairs - 1) / pairs * (256 + bn);
         if (best_cost < 0 || cost < best_cost) {
             best = bn;
             best_cost = cost;
