@@ -17,6 +17,10 @@
 // exactly, by 64-bit keys (logit, then lowest index).  Where ties make them too many (a row of equal logits), the
 // bound is found exactly, over logits and then over indexes, by more such readings.
 // Nothing synchronises warps, so one's selection runs beside the others' streams.
+//
+// 64 requests of 8 beams x 248,320 bf16 logits, 16 results: 63 us (4.0 TB/s), 57 of it the
+// slices (without the exponentials 8 us less, without the selection 11); blocks of 8 warps
+// that synchronise took 71.  One request of 4 beams: 12 us, half of it the merge.
 #pragma once
 
 #include "device.cuh"

