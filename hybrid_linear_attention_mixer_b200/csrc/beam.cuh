@@ -214,9 +214,10 @@ __device__ __forceinline__ uint4 load_vec(const T* x, int i0, int V, int shift) 
     return u;
 }
 
-// A bound that at least n of the SETS maxima reach and not many more (n + 8, but for
-// ties); each lane holds GROUPS of them.  -FLT_MAX where no more than n are above -inf.
-__device__ __forceinline__ float find_bound(const float (&mine)[GROUPS], float top, int n) {
+// A bound that at least n of the SETS maxima reach and not many more (n + 8; where ties
+// make them more, fewer than n are above it, and tied is set); each lane holds GROUPS of
+// them.  -FLT_MAX where no more than n are above -inf.
+__device__ __forceinline__ float find_bound(const float (&mine)[GROUPS], float top, int n, bool& tied) {
     int valid = 0;
     uint32_t least = 0xffffffffu;
 #pragma unroll
@@ -228,6 +229,7 @@ __device__ __forceinline__ float find_bound(const float (&mine)[GROUPS], float t
     }
     valid = __reduce_add_sync(0xffffffffu, valid);
     least = __reduce_min_sync(0xffffffffu, least);
+    tied = false;
     if (valid <= n) return -3.402823466e38f;
     uint32_t lo = least, hi = ordered(top);   // at least n reach lo, fewer reach anything above hi
     int at_lo = valid;
@@ -245,6 +247,7 @@ __device__ __forceinline__ float find_bound(const float (&mine)[GROUPS], float t
             hi = mid - 1;
         }
     }
+    tied = at_lo > n + 8;
     return from_ordered(lo);
 }
 
@@ -382,35 +385,74 @@ __global__ void __launch_bounds__(WARPS * 32, 32 / WARPS) slice_kernel(const __g
         s_n = 0;
     }
 
-    // the tile maxima that reach the bound, and of the vectors behind them the logits that do
-    float bound = find_bound(mine, top, p.n);
-    int listed = 0;
+    // The tile maxima that reach the bound, and of the vectors behind them the logits that do;
+    // if those are too many to hold because of ties, the ones above the bound.
+    bool tied;
+    float bound = find_bound(mine, top, p.n, tied);
+    float low = bound;
+    bool held;
+#pragma unroll 1
+    while (true) {
+        int listed = 0;
 #pragma unroll 4
-    for (int t = 0; t < tiles; ++t) {
-        const bool mine_hits = s_top[32 * t] >= bound;
-        const uint32_t hit = __ballot_sync(kAll, mine_hits);
-        const int k = listed + __popc(hit & ((1u << lane) - 1u));
-        if (mine_hits && k < LISTED) s_list[k] = (uint16_t)(t * 32 + lane);
-        listed += __popc(hit);
-    }
-    __syncwarp();
-    for (int i = lane; i < min(listed, LISTED) * VPT; i += 32) {
-        const int set = s_list[i / VPT];
-        const int i0 = begin + set / 32 * kTile + i % VPT * kStep + set % 32 * N;
-        const uint4 u[1] = {load_vec<T>(x, i0, p.V, shift)};
-        if (X::top(u) >= bound) {
+        for (int t = 0; t < tiles; ++t) {
+            const bool hits = s_top[32 * t] >= low;
+            const uint32_t hit = __ballot_sync(kAll, hits);
+            const int k = listed + __popc(hit & ((1u << lane) - 1u));
+            if (hits && k < LISTED) s_list[k] = (uint16_t)(t * 32 + lane);
+            listed += __popc(hit);
+        }
+        __syncwarp();
+        for (int i = lane; i < min(listed, LISTED) * VPT; i += 32) {
+            const int set = s_list[i / VPT];
+            const int i0 = begin + set / 32 * kTile + i % VPT * kStep + set % 32 * N;
+            const uint4 u[1] = {load_vec<T>(x, i0, p.V, shift)};
+            if (X::top(u) >= low) {
 #pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const float f = X::get(u[0], e);
-                if (f >= bound) {
-                    const int k = atomicAdd(&s_n, 1);
-                    if (k < CAP) s_key[k] = make_key(f, i0 + e);
+                for (int e = 0; e < N; ++e) {
+                    const float f = X::get(u[0], e);
+                    if (f >= low) {
+                        const int k = atomicAdd(&s_n, 1);
+                        if (k < CAP) s_key[k] = make_key(f, i0 + e);
+                    }
                 }
             }
         }
+        __syncwarp();
+        held = listed <= LISTED && s_n <= CAP;
+        if (held || !tied || low > bound) break;
+        low = from_ordered(ordered(bound) + 1u);   // the next number
+        __syncwarp();
+        if (lane == 0) s_n = 0;
+        __syncwarp();
     }
-    __syncwarp();
-    if (listed > LISTED || s_n > CAP) {
+    if (low > bound) {   // of those equal to the bound, the first n
+        int have = 0;   // logits equal to the bound so far
+#pragma unroll 1
+        for (int j = 0; j < tiles * VPT && have < p.n; ++j) {   // 32 vectors in a row
+            const uint4 u = vec(j);
+            int mine_eq = 0;
+#pragma unroll
+            for (int e = 0; e < N; ++e) mine_eq += X::get(u, e) == bound;
+            int upto = mine_eq;   // this lane's and those of the lanes before
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int v = __shfl_up_sync(kAll, upto, d);
+                if (lane >= d) upto += v;
+            }
+            int order = have + upto - mine_eq;
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                if (X::get(u, e) == bound && order++ < p.n) {
+                    const int k = atomicAdd(&s_n, 1);
+                    if (k < CAP) s_key[k] = make_key(bound, first + j * kStep + e);
+                }
+            have += __shfl_sync(kAll, upto, 31);
+        }
+        __syncwarp();
+        held = held && s_n <= CAP;
+    }
+    if (!held) {
         // Too many reach it.  The n-th largest logit itself ...
         auto each = [&](auto&& use) {   // use(value, index) for the lane's logits
 #pragma unroll 1

@@ -212,7 +212,9 @@ template <int BT, int kSplits>
 struct RowsForm {
     using S = gdn::gemm::RowsShape<BT>;
     static constexpr auto kernel = gdn::gemm::linear_i8_rows_kernel<BT, kSplits>;
-    static int at_once() { return resident_clusters<kernel>(kSplits, gdn::gemm::NT, S::SMEM); }
+    static int at_once() {   // (the runtime counts what the kernel is allowed)
+        return allow_smem<kernel>(S::SMEM) == cudaSuccess ? resident_clusters<kernel>(kSplits, gdn::gemm::NT, S::SMEM) : 0;
+    }
     static cudaError_t launch(const CUtensorMap& tm_x, const CUtensorMap& tm_w, const gdn::gemm::I8Args& a,
                               cudaStream_t st) {
         const cudaError_t e = allow_smem<kernel>(S::SMEM);

@@ -435,6 +435,36 @@ def test_beam_select_ties(dt, V):
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1, 7, 30])
+def test_beam_select_many_ties_below_a_few(dt, n):
+    """A few distinct logits above, then thousands of equal ones spread over the row; the
+    equal ones everywhere but at its start; and equal ones that are fewer than n."""
+    W, V = 2, 70000
+    rng = np.random.default_rng(17)
+    x = np.full((3, W, V), -3.0)
+    x[0] = np.where(rng.random((W, V)) < 0.1, 4.0, rng.integers(-12, 4, (W, V)))
+    x[1, :, 60000:] = 2.5
+    x[1, :, :60000] = rng.integers(-9, 0, (W, 60000))
+    for w in range(W):
+        x[:, w, rng.permutation(V)[:12]] = 8 + np.arange(12) * 0.25
+    x[2, :, rng.permutation(V)[:5]] = 6.0
+    logits, scores = on(x, dt), torch.zeros((3, W), device=DEV)
+    # Two beams with the same logits in another order have the same sum of exponentials but for
+    # its rounding, within BEAM_ERR: which of their equal candidates comes first is not said.
+    # Their scores are.
+    _, _, s = gdn.beam_select(logits, scores, n_out=n)
+    ref = S.beam_select(logits.cpu().float().numpy(), np.zeros((3, W)), n)[2]
+    assert worst(np.abs(f64(s) - ref), S.BEAM_ERR + 2 * S.U32 * np.abs(ref)) <= 1
+    # each beam by itself, where nothing but the logits decides
+    for w in range(W):
+        one = logits[:, w:w + 1].contiguous()
+        p, t, _ = gdn.beam_select(one, scores[:, :1].contiguous(), n_out=n)
+        ref = S.beam_select(one.cpu().float().numpy(), np.zeros((3, 1)), n)
+        np.testing.assert_array_equal(p.cpu().numpy(), ref[0])
+        np.testing.assert_array_equal(t.cpu().numpy(), ref[1])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_beam_select_row_starts(dt):
     """Rows at every offset within 16 bytes, and rows further apart than the vocabulary."""
     W, V, n = 4, 16411, 8
