@@ -27,6 +27,7 @@ struct I8Args : Args {
     const float* w_scale;
     int out_f32;           // destinations are fp32 (else bf16)
     int w_ready;           // the kernel before this one does not write w
+    int tile_rows;         // channels of a tile (rows kernel): a multiple of 8, at most 128
 };
 
 #define GDN_ELECT "{\n\t.reg .pred e;\n\t.reg .b32 ex;\n\telect.sync ex|e, 0xffffffff;\n\t"
@@ -143,9 +144,11 @@ struct I8Op {
 };
 
 // ---------------------------------------------------------------------------
-// Few tokens: the weights' rows are the MMA's M (128 channels a tile), the tokens
+// Few tokens: the weights' rows are the MMA's M (up to 128 channels a tile), the tokens
 // its N (BT = 16 .. 128, rows past M read as zeros), so a tile's time is that of
-// its 16 KiB of weights per k-block and the tokens cost little.  One persistent
+// its 16 KiB of weights per k-block and the tokens cost little.  A tile takes fewer channels
+// where that deals them out evenly over the SMs (the MMA's rows past them hold whatever the
+// stage held and are not read).  One persistent
 // CTA per SM with the roles of linear_kernel: TMA producer, MMA issuer, 4 epilogue
 // warps over two TMEM accumulators; the ring holds about 200 KiB in flight, several
 // times what an SM needs to draw its share of HBM.
@@ -242,15 +245,16 @@ linear_i8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
             const uint32_t pre = total < (uint32_t)S::STAGES ? total : S::STAGES;
             auto load_w = [&](uint32_t it, int s) {
                 const int tile = first + (int)(it / kb_n) * step, kb = k_lo + (int)(it % kb_n);
-                tma_load_2d(sb + (uint32_t)s * S::STAGE, &tm_w, kb * BK8, tile * 128, full(s));
+                tma_load_2d(sb + (uint32_t)s * S::STAGE, &tm_w, kb * BK8, tile * p.tile_rows, full(s));
             };
             auto load_x = [&](uint32_t it, int s) {
                 const int kb = k_lo + (int)(it % kb_n);
                 tma_load_2d(sb + (uint32_t)s * S::STAGE + S::W_BYTES, &tm_x, kb * BK8, 0, full(s));
             };
+            const uint32_t bytes = (uint32_t)(p.tile_rows * BK8 + S::X_BYTES);   // of a stage
             if (!p.w_ready) grid_dependency_wait();
             for (uint32_t it = 0; it < pre; ++it) {
-                mbar_arrive_expect_tx(full(it), S::STAGE);
+                mbar_arrive_expect_tx(full(it), bytes);
                 load_w(it, it);
             }
             if (p.w_ready) grid_dependency_wait();
@@ -263,7 +267,7 @@ linear_i8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
                     ok = false;
                     break;
                 }
-                mbar_arrive_expect_tx(full(s), S::STAGE);
+                mbar_arrive_expect_tx(full(s), bytes);
                 load_w(it, s);
                 load_x(it, s);
             }
@@ -325,7 +329,7 @@ linear_i8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
         bool ok = true;
         for (int ti = 0; ti < my_tiles; ++ti) {
             const uint32_t a = ti & 1u;
-            const int n = (first + ti * step) * 128 + row;
+            const int n = row < p.tile_rows ? (first + ti * step) * p.tile_rows + row : p.N;
             const float ws = n < p.N ? p.w_scale[n] : 0.0f;
             const Seg& sg = segment_of(p, n);
             if (!mbar_wait_bounded(acc_full(a), (ti >> 1) & 1u) || *s_abort) {
@@ -369,7 +373,7 @@ linear_i8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
         // One tile per cluster.  CTA m % kSplits adds up token m, a warp to a token and a
         // lane to four channels.
         cluster_sync();
-        const int n = first * 128 + lane * 4;
+        const int n = lane * 4 < p.tile_rows ? first * p.tile_rows + lane * 4 : p.N;
         if (warp >= 2 && !*s_abort && my_tiles > 0 && n < p.N) {
             const float* xs = reinterpret_cast<const float*>(smem + S::OFF_XS);
             const Seg& sg = segment_of(p, n);

@@ -208,6 +208,8 @@ int pick_bn_i8(int64_t M, int N, int pairs) {
     return best;
 }
 
+constexpr int kMinTileRows = 96, kJoinCost = 250;
+
 template <int BT, int kSplits>
 struct RowsForm {
     using S = gdn::gemm::RowsShape<BT>;
@@ -226,22 +228,30 @@ struct RowsForm {
 
 template <int BT>
 cudaError_t launch_i8_rows(const void* x, const void* w, gdn::gemm::I8Args a, cudaStream_t st) {
-    CUtensorMap tm_x, tm_w;
-    if (!i8_map(&tm_x, x, a.M, a.K, BT) || !i8_map(&tm_w, w, a.N, a.K, 128)) return cudaErrorInvalidValue;
-    a.n_blocks = (a.N + 127) / 128;
-    // Split K where the tiles leave SMs idle (one tile per cluster): the k-blocks that the
-    // busiest CTA walks, and a few more for the join.
+    // Tile height and split of K: the fewest bytes (of 128) that one CTA loads, over the
+    // clusters that run at once; a split (one tile per cluster) pays for its join.  Heights
+    // below 128 even out the waves (64 rows x 64,000 outputs x 2560: 29.7 us, 31.7 with 128).
     const int kb = (a.K + gdn::gemm::BK8 - 1) / gdn::gemm::BK8;
     const int at_once[4] = {sm_count(), RowsForm<BT, 2>::at_once(), RowsForm<BT, 4>::at_once(), RowsForm<BT, 8>::at_once()};
     int best = 0;
-    int64_t best_cost = (int64_t)((a.n_blocks + at_once[0] - 1) / at_once[0]) * kb;
-    for (int i = 1; i < 4 && (1 << i) <= kb && a.n_blocks <= at_once[i]; ++i) {
-        const int64_t cost = (kb + (1 << i) - 1) / (1 << i) + 4;
-        if (cost < best_cost) {
-            best_cost = cost;
-            best = i;
+    int64_t best_cost = INT64_MAX;
+    for (int i = 0; i < 4 && (1 << i) <= kb; ++i) {
+        if (at_once[i] <= 0) break;
+        for (int rows = 128; rows >= kMinTileRows; rows -= 8) {
+            const int tiles = (a.N + rows - 1) / rows;
+            if (i > 0 && tiles > at_once[i]) break;
+            const int64_t cost = (int64_t)((tiles + at_once[i] - 1) / at_once[i]) * (rows + BT) * ((kb + (1 << i) - 1) >> i) +
+                                 (i > 0 ? kJoinCost : 0);
+            if (cost < best_cost) {
+                best_cost = cost;
+                best = i;
+                a.tile_rows = rows;
+                a.n_blocks = tiles;
+            }
         }
     }
+    CUtensorMap tm_x, tm_w;
+    if (!i8_map(&tm_x, x, a.M, a.K, BT) || !i8_map(&tm_w, w, a.N, a.K, a.tile_rows)) return cudaErrorInvalidValue;
     switch (best) {
         case 0: return RowsForm<BT, 1>::launch(tm_x, tm_w, a, st);
         case 1: return RowsForm<BT, 2>::launch(tm_x, tm_w, a, st);

@@ -440,22 +440,24 @@ def cp_finish(cfg: Config, w: dict, z, summaries, rank: int, state_in, workspace
 # ---------------------------------------------------------------------------
 # The operators around the mixer in a serving step
 # ---------------------------------------------------------------------------
-def _device_of(t, name):
-    if not t.is_cuda:
+def _index_of(t, name) -> int:
+    """The index of the CUDA device that t is on."""
+    index = t.get_device()
+    if index < 0:
         raise ValueError("%s must be a CUDA tensor" % name)
-    return t.device
+    return index
 
 
-def _shaped(t, name, dtype, device, *shape):
-    """A contiguous tensor of this dtype, device and shape: its address."""
-    if t.dtype is dtype and t.shape == shape and t.get_device() == device.index and t.is_contiguous():
+def _shaped(t, name, dtype, index, shape):
+    """A contiguous tensor of this dtype, CUDA device and shape: its address."""
+    if t.dtype is dtype and t.get_device() == index and t.shape == shape and t.is_contiguous():
         return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError("%s: dtype %s, expected %s" % (name, t.dtype, dtype))
     if t.shape != shape:
         raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), shape))
-    if t.device != device:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.get_device() != index:
+        raise ValueError("%s is on %s, expected cuda:%d" % (name, t.device, index))
     raise ValueError("%s must be contiguous" % name)
 
 
@@ -466,24 +468,24 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _call(fn, what, device, stream, *args):
+def _call(fn, what, index, stream, *args):
     """fn(*args, stream) on the tensors' device, which need not be the current one.  The
     stream is the caller's, else that device's current one."""
-    if _current_device() != device.index:
-        with torch.cuda.device(device):
-            return _call(fn, what, device, stream, *args)
-    s = fn(*args, _raw_stream(device.index) if stream is None else stream.cuda_stream)
+    if _current_device() != index:
+        with torch.cuda.device(index):
+            return _call(fn, what, index, stream, *args)
+    s = fn(*args, _raw_stream(index) if stream is None else stream.cuda_stream)
     if s != 0:
         raise GdnError(s, what)
 
 
-def _empty(shape, dtype, device, stream):
+def _empty(shape, dtype, index, stream):
     """Memory for the call to use on ``stream``: taken from that stream's pool, so that
     neither its last user nor its next can still be at work on another stream."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=index)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=index)
 
 
 _GATES = {"none": 0, "token": 1, "channel": 2, "full": 3}
@@ -517,37 +519,37 @@ def block_norm(cfg: NormConfig, o, x, gate=None, w_post=None, w_pre=None, r=None
     w_post / w_pre [dim] float32 (None: no norm after / no y).  ``r`` may be x and ``y``
     may be o.  With ``quantize``, or where ``y_scale`` [T] is given, y is int8 rows.
     Returns (r, y, y_scale), None for what there is not."""
-    dev = _device_of(x, "x")
+    dev = _index_of(x, "x")
     T, D = x.shape[0], cfg.dim
     act, res = cfg.act_dtype, cfg.res_dtype
-    px = _shaped(x, "x", res, dev, T, D)
+    px = _shaped(x, "x", res, dev, (T, D))
     po = pg = pp = pw = pr = py = ps = None
     if o is not None:
-        po = _shaped(o, "o", act, dev, T, D)
+        po = _shaped(o, "o", act, dev, (T, D))
         if r is None:
             r = _empty((T, D), res, dev, stream)
-        pr = _shaped(r, "r", res, dev, T, D)
+        pr = _shaped(r, "r", res, dev, (T, D))
     elif r is not None:
         raise ValueError("r without a block output o")
     if gate is not None:
         if cfg.gate == "channel":
-            pg = _shaped(gate, "gate", torch.float32, dev, D)
+            pg = _shaped(gate, "gate", torch.float32, dev, (D,))
         elif cfg.gate == "token":
-            pg = _shaped(gate, "gate", act, dev, T)
+            pg = _shaped(gate, "gate", act, dev, (T,))
         else:
-            pg = _shaped(gate, "gate", act, dev, T, D)
+            pg = _shaped(gate, "gate", act, dev, (T, D))
     if w_post is not None:
-        pp = _shaped(w_post, "w_post", torch.float32, dev, D)
+        pp = _shaped(w_post, "w_post", torch.float32, dev, (D,))
     if w_pre is not None:
-        pw = _shaped(w_pre, "w_pre", torch.float32, dev, D)
+        pw = _shaped(w_pre, "w_pre", torch.float32, dev, (D,))
         if y_scale is not None or quantize:
             if y_scale is None:
                 y_scale = _empty(T, torch.float32, dev, stream)
-            ps = _shaped(y_scale, "y_scale", torch.float32, dev, T)
+            ps = _shaped(y_scale, "y_scale", torch.float32, dev, (T,))
         y_dtype = torch.int8 if ps is not None else act
         if y is None:
             y = _empty((T, D), y_dtype, dev, stream)
-        py = _shaped(y, "y", y_dtype, dev, T, D)
+        py = _shaped(y, "y", y_dtype, dev, (T, D))
     elif y is not None or y_scale is not None or quantize:
         raise ValueError("y without w_pre")
     _call(lib().gdn_block_norm, "gdn_block_norm", dev, stream, cfg.ref(), po, px, pg, pp, pw, T, pr, py, ps)
@@ -558,19 +560,19 @@ def quantize_rows(x, q=None, scale=None, stream=None):
     """Rows in 8-bit integers: x [rows, cols] bf16 or float32 -> (q int8 [rows, cols],
     scale float32 [rows]) with x ~ scale * q.  For activations a row is a token; for a
     linear layer's weight it is an output channel."""
-    dev = _device_of(x, "x")
+    dev = _index_of(x, "x")
     if x.dim() != 2:
         raise ValueError("x [rows, cols] expected, got %s" % (tuple(x.shape),))
     rows, cols = x.shape
     if x.dtype not in _DT:
         raise TypeError("x: dtype %s, expected bfloat16 or float32" % x.dtype)
-    px = _shaped(x, "x", x.dtype, dev, rows, cols)
+    px = _shaped(x, "x", x.dtype, dev, (rows, cols))
     if q is None:
         q = _empty((rows, cols), torch.int8, dev, stream)
     if scale is None:
         scale = _empty(rows, torch.float32, dev, stream)
     _call(lib().gdn_quantize_rows, "gdn_quantize_rows", dev, stream, px, _DT[x.dtype], rows, cols,
-          _shaped(q, "q", torch.int8, dev, rows, cols), _shaped(scale, "scale", torch.float32, dev, rows))
+          _shaped(q, "q", torch.int8, dev, (rows, cols)), _shaped(scale, "scale", torch.float32, dev, (rows,)))
     return q, scale
 
 
@@ -584,21 +586,21 @@ def _i8_operand(x, x_scale, name, dev, M, K, workspace, stream):
     if x.dtype == torch.int8:
         if x_scale is None:
             raise ValueError("%s in int8 needs its scales" % name)
-        return (_shaped(x, name, torch.int8, dev, M, K), _I8,
-                _shaped(x_scale, name + "_scale", torch.float32, dev, M), None, 0, None)
+        return (_shaped(x, name, torch.int8, dev, (M, K)), _I8,
+                _shaped(x_scale, name + "_scale", torch.float32, dev, (M,)), None, 0, None)
     if x_scale is not None:
         raise ValueError("%s_scale is for int8 rows; %s is %s" % (name, name, x.dtype))
     if x.dtype not in _DT:
         raise TypeError("%s: dtype %s, expected bfloat16, float32 or int8" % (name, x.dtype))
-    px = _shaped(x, name, x.dtype, dev, M, K)
+    px = _shaped(x, name, x.dtype, dev, (M, K))
     if workspace is None:
         workspace = _empty(linear_i8_workspace_size(M, K), torch.uint8, dev, stream)
     return px, _DT[x.dtype], None, _workspace(workspace, dev), workspace.numel(), workspace
 
 
 def _workspace(t, dev):
-    if t.dtype is not torch.uint8 or t.get_device() != dev.index or not t.is_contiguous():
-        raise ValueError("workspace must be contiguous uint8 on %s" % dev)
+    if t.dtype is not torch.uint8 or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError("workspace must be contiguous uint8 on cuda:%d" % dev)
     return t.data_ptr()
 
 
@@ -608,7 +610,7 @@ def linear_i8(x, w, w_scale, x_scale=None, outs=None, out_dtype=torch.bfloat16, 
     call makes int8 first (``workspace``: linear_i8_workspace_size bytes of uint8).  ``outs``
     as in ``linear`` (bf16, or all float32); default one [M, N] tensor of ``out_dtype``.
     Returns the list of outputs."""
-    dev = _device_of(x, "x")
+    dev = _index_of(x, "x")
     if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
         raise ValueError("x [M, K] and w [N, K] expected, got %s and %s" % (tuple(x.shape), tuple(w.shape)))
     M, K = x.shape
@@ -624,11 +626,11 @@ def linear_i8(x, w, w_scale, x_scale=None, outs=None, out_dtype=torch.bfloat16, 
     for i, o in enumerate(outs):
         if o.dim() != 2:
             raise ValueError("outs[%d] must be [M, width]" % i)
-        segs[i].dst = _shaped(o, "outs[%d]" % i, dt, dev, M, o.shape[1])
+        segs[i].dst = _shaped(o, "outs[%d]" % i, dt, dev, (M, o.shape[1]))
         segs[i].width = o.shape[1]
     px, xdt, pxs, ws, ws_bytes, workspace = _i8_operand(x, x_scale, "x", dev, M, K, workspace, stream)
-    _call(lib().gdn_linear_i8, "gdn_linear_i8", dev, stream, px, xdt, pxs, _shaped(w, "w", torch.int8, dev, N, K),
-          _shaped(w_scale, "w_scale", torch.float32, dev, N), M, N, K, _DT[dt], segs, len(outs), ws, ws_bytes)
+    _call(lib().gdn_linear_i8, "gdn_linear_i8", dev, stream, px, xdt, pxs, _shaped(w, "w", torch.int8, dev, (N, K)),
+          _shaped(w_scale, "w_scale", torch.float32, dev, (N,)), M, N, K, _DT[dt], segs, len(outs), ws, ws_bytes)
     return outs
 
 
@@ -636,18 +638,18 @@ def in_proj_i8(cfg: Config, hidden, w_in, w_scale, hidden_scale=None, out: dict 
                stream=None) -> dict:
     """The mixer's input projection in 8-bit integers: ``in_proj`` with w_in int8 and its
     scales [rows of w_in]; hidden as x in ``linear_i8``."""
-    dev = _device_of(hidden, "hidden")
+    dev = _index_of(hidden, "hidden")
     T, D = hidden.shape
     qk, vz, ab = cfg.n_k_heads * cfg.d_k, cfg.n_v_heads * cfg.d_v, cfg.n_v_heads
     N = 2 * qk + 2 * vz + 2 * ab
     widths = (("q", qk), ("k", qk), ("v", vz), ("z", vz), ("a", ab), ("b", ab))
-    pw, pws = _shaped(w_in, "w_in", torch.int8, dev, N, D), _shaped(w_scale, "w_scale", torch.float32, dev, N)
+    pw, pws = _shaped(w_in, "w_in", torch.int8, dev, (N, D)), _shaped(w_scale, "w_scale", torch.float32, dev, (N,))
     o = out if out is not None else {n: _empty((T, wd), torch.bfloat16, dev, stream) for n, wd in widths}
     ptrs = []
     for n, wd in widths:   # (flat or by heads, as for in_proj)
         t = o[n]
-        if t.dtype is not torch.bfloat16 or t.get_device() != dev.index or not t.is_contiguous():
-            _check(t, n, torch.bfloat16, dev)
+        if t.dtype is not torch.bfloat16 or t.get_device() != dev or not t.is_contiguous():
+            _check(t, n, torch.bfloat16, hidden.device)
         if t.numel() != T * wd:
             raise ValueError("%s must hold [T, %d]" % (n, wd))
         ptrs.append(t.data_ptr())
@@ -660,15 +662,15 @@ def in_proj_i8(cfg: Config, hidden, w_in, w_scale, hidden_scale=None, out: dict 
 def out_proj_i8(cfg: Config, o, w_out, w_scale, o_scale=None, y=None, workspace=None, stream=None):
     """The mixer's output projection in 8-bit integers: ``out_proj`` with w_out int8 and its
     scales [d_model]; o as x in ``linear_i8``.  y [T, d_model] bf16."""
-    dev = _device_of(o, "o")
+    dev = _index_of(o, "o")
     o2 = o.reshape(o.shape[0], -1) if o.is_contiguous() else o
     T, K, D = o2.shape[0], cfg.n_v_heads * cfg.d_v, w_out.shape[0]
     if y is None:
         y = _empty((T, D), torch.bfloat16, dev, stream)
     px, xdt, pxs, ws, ws_bytes, workspace = _i8_operand(o2, o_scale, "o", dev, T, K, workspace, stream)
     _call(lib().gdn_out_proj_i8, "gdn_out_proj_i8", dev, stream, cfg.ref(), px, xdt, pxs,
-          _shaped(w_out, "w_out", torch.int8, dev, D, K), _shaped(w_scale, "w_scale", torch.float32, dev, D), T, D,
-          _shaped(y, "y", torch.bfloat16, dev, T, D), ws, ws_bytes)
+          _shaped(w_out, "w_out", torch.int8, dev, (D, K)), _shaped(w_scale, "w_scale", torch.float32, dev, (D,)), T, D,
+          _shaped(y, "y", torch.bfloat16, dev, (T, D)), ws, ws_bytes)
     return y
 
 
@@ -687,7 +689,7 @@ def beam_select(logits, scores, n_out=None, finished=None, pad_token=0, parents=
     (such a beam goes on with ``pad_token`` and its score).  Returns (parents, tokens,
     scores), each [groups, n_out]; -1, -1, -inf where there are fewer candidates.
     ``out_scores`` may be ``scores`` when n_out is the number of beams."""
-    dev = _device_of(logits, "logits")
+    dev = _index_of(logits, "logits")
     if logits.dim() != 3:
         raise ValueError("logits [groups, beams, vocab] expected, got %s" % (tuple(logits.shape),))
     G, W, V = logits.shape
@@ -703,7 +705,7 @@ def beam_select(logits, scores, n_out=None, finished=None, pad_token=0, parents=
             raise ValueError("logits: rows must be dense and evenly spaced, strides %s" % (logits.stride(),))
     pf = None
     if finished is not None:
-        pf = _shaped(finished, "finished", torch.bool if finished.dtype == torch.bool else torch.uint8, dev, G, W)
+        pf = _shaped(finished, "finished", torch.bool if finished.dtype == torch.bool else torch.uint8, dev, (G, W))
     if parents is None:
         parents = _empty((G, n_out), torch.int32, dev, stream)
     if tokens is None:
@@ -713,9 +715,9 @@ def beam_select(logits, scores, n_out=None, finished=None, pad_token=0, parents=
     if workspace is None:
         workspace = _empty(beam_workspace_size(G, W, V, n_out, logits.dtype), torch.uint8, dev, stream)
     _call(lib().gdn_beam_select, "gdn_beam_select", dev, stream, logits.data_ptr(), dt, ld,
-          _shaped(scores, "scores", torch.float32, dev, G, W), pf, G, W, V, n_out, pad_token,
-          _shaped(parents, "parents", torch.int32, dev, G, n_out), _shaped(tokens, "tokens", torch.int32, dev, G, n_out),
-          _shaped(out_scores, "out_scores", torch.float32, dev, G, n_out), _workspace(workspace, dev), workspace.numel())
+          _shaped(scores, "scores", torch.float32, dev, (G, W)), pf, G, W, V, n_out, pad_token,
+          _shaped(parents, "parents", torch.int32, dev, (G, n_out)), _shaped(tokens, "tokens", torch.int32, dev, (G, n_out)),
+          _shaped(out_scores, "out_scores", torch.float32, dev, (G, n_out)), _workspace(workspace, dev), workspace.numel())
     return parents, tokens, out_scores
 
 
@@ -726,11 +728,11 @@ class ReorderPlan:
         if not 0 < len(states) <= REORDER_MAX_BUFFERS:
             raise ValueError("1..%d states" % REORDER_MAX_BUFFERS)
         self.states, self.n_groups, self.n_beams = list(states), int(n_groups), int(n_beams)
-        self.device = _device_of(states[0], "states[0]")
+        self.device = _index_of(states[0], "states[0]")
         self.buffers = (_CStateBuffer * len(states))()
         for i, t in enumerate(self.states):
-            if t.device != self.device:
-                raise ValueError("states[%d] is on %s, expected %s" % (i, t.device, self.device))
+            if t.get_device() != self.device:
+                raise ValueError("states[%d] is on %s, expected cuda:%d" % (i, t.device, self.device))
             if t.dim() < 2 or t.shape[0] != self.n_groups * self.n_beams:
                 raise ValueError("states[%d]: shape %s, expected [%d, ...]"
                                  % (i, tuple(t.shape), self.n_groups * self.n_beams))
@@ -761,7 +763,7 @@ def reorder_states(parents, states, stream=None) -> None:
         states = ReorderPlan(states, *parents.shape)
     dev = states.device
     _call(lib().gdn_reorder_states, "gdn_reorder_states", dev, stream,
-          _shaped(parents, "parents", torch.int32, dev, states.n_groups, states.n_beams), states.n_groups,
+          _shaped(parents, "parents", torch.int32, dev, (states.n_groups, states.n_beams)), states.n_groups,
           states.n_beams, states.buffers, len(states.buffers))
 
 
