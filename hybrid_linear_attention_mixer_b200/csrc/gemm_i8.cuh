@@ -11,6 +11,7 @@
 #pragma once
 
 #include "gemm.cuh"
+#include "quant.cuh"
 
 namespace gdn {
 namespace gemm {
@@ -28,6 +29,8 @@ struct I8Args : Args {
     int out_f32;           // destinations are fp32 (else bf16)
     int w_ready;           // the kernel before this one does not write w
     int tile_rows;         // channels of a tile (rows kernel): a multiple of 8, at most 128
+    const void* x_raw;     // rows that the rows kernel makes 8-bit itself, bf16 or fp32
+    int x_f32;
 };
 
 #define GDN_ELECT "{\n\t.reg .pred e;\n\t.reg .b32 ex;\n\telect.sync ex|e, 0xffffffff;\n\t"
@@ -159,22 +162,79 @@ struct I8Op {
 // Launched behind the kernel that makes the 8-bit rows: the weights, which that
 // kernel does not write, are fetched while it still runs.
 // ---------------------------------------------------------------------------
-template <int BT>
+// One bf16 or fp32 token, or two short ones (XQ > 0: the most k-blocks of a row): every CTA
+// makes them 8-bit itself while its first weights are on their way, into shared memory; that
+// saves the launch before.  One token x 16480 x 2560: 9.2 us, 10.4 with that launch, x 64000:
+// 25.5 and 28.3; two rows of 6144 lose by it (8.5 and 7.5 for 2560 outputs), and so do more
+// rows.
+template <int BT, int XQ>
 struct RowsShape {
     static_assert(BT % 16 == 0 && BT >= 16 && BT <= 128, "tokens a tile");
     static constexpr int W_BYTES = 128 * BK8;
-    static constexpr int X_BYTES = BT * BK8;
+    static constexpr int X_BYTES = XQ ? 0 : BT * BK8;
     static constexpr int STAGE = W_BYTES + X_BYTES;
-    static constexpr int STAGES = (200 * 1024) / STAGE;
-    static constexpr int OFF_BAR = STAGES * STAGE;
-    static constexpr int N_BARS = 2 * STAGES + 5;   // full, empty, acc_full[2], acc_empty[2], drain
+    static constexpr int XQ_BYTES = XQ * BT * BK8;
+    static constexpr int STAGES = (200 * 1024 - XQ_BYTES) / STAGE;
+    static constexpr int OFF_XQ = STAGES * STAGE;
+    static constexpr int OFF_BAR = OFF_XQ + XQ_BYTES;
+    static constexpr int N_BARS = 2 * STAGES + 6;   // full, empty, acc_full[2], acc_empty[2], drain, x_ready
     static constexpr int OFF_XS = (OFF_BAR + N_BARS * 8 + 8 + 15) & ~15;   // x_scale of the BT tokens
     static constexpr int SMEM = OFF_XS + BT * 4 + 1024;
     static constexpr uint32_t TMEM_COLS = 2 * BT < 32 ? 32 : 2 * BT;
-    static_assert(STAGE % 1024 == 0, "stage alignment");
+    static_assert(STAGE % 1024 == 0 && XQ_BYTES % 1024 == 0, "swizzle atoms");
     static_assert(SMEM <= 227 * 1024, "shared memory");
     static_assert(STAGES * STAGE >= BT * 128 * 4, "partial sums fit where the stages were");
 };
+// What a thread of the 128 holds of the raw rows in registers.
+template <int XQ>
+struct RawShape {
+    static constexpr int ROWS = XQ <= 24 ? 2 : 1, VECS = XQ / 8;
+};
+
+// All rows of x (at most R, of at most 1024 NV elements) as 8-bit integers, k-blocks
+// [k_lo, k_lo + kb_n) of them into shared memory in the layout that a load by tensor map
+// leaves, by the four epilogue warps (thread t of 128).  xs: the rows' scales; its upper half
+// is scratch.
+template <typename T, int R, int NV>
+__device__ __forceinline__ void raw_rows_to_i8(const T* x, int M, int K, int k_lo, int kb_n, uint8_t* xq, int tile_bytes,
+                                               float* xs, int t) {
+    constexpr int kVecs = BK8 / 8;   // of a k-block
+    const int nv = K / 8;
+    uint32_t* part = reinterpret_cast<uint32_t*>(xs + 8);
+    quant::Raw8<T> v[R][NV];
+#pragma unroll
+    for (int m = 0; m < R; ++m)
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (m < M && t + j * 128 < nv) v[m][j].load(x + (int64_t)m * K + 8 * (t + j * 128));
+#pragma unroll
+    for (int m = 0; m < R; ++m) {
+        uint32_t amax = 0;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (m < M && t + j * 128 < nv) amax = max(amax, v[m][j].max_bits());
+        amax = __reduce_max_sync(0xffffffffu, amax);
+        if ((t & 31) == 0) part[m * 4 + (t >> 5)] = amax;
+    }
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    const int lo = k_lo * kVecs, hi = lo + kb_n * kVecs;
+#pragma unroll
+    for (int m = 0; m < R; ++m) {
+        if (m >= M) break;
+        const uint32_t* q = part + m * 4;
+        const quant::RowScale s = quant::row_scale(max(max(q[0], q[1]), max(q[2], q[3])));
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int i = t + j * 128;
+            if (i >= nv || i < lo || i >= hi) continue;
+            float f[8];
+            v[m][j].get(f);
+            const int kb = (i - lo) / kVecs, k8 = (i - lo) % kVecs;
+            *reinterpret_cast<uint2*>(xq + kb * tile_bytes + swz128(m, k8 >> 1) + (k8 & 1) * 8) = quant::pack_i8(f, s);
+        }
+        if (t == 0) xs[m] = s.scale;
+    }
+}
 
 __device__ __forceinline__ int4 ld_cluster_int4(uint32_t addr) {
     int4 v;
@@ -185,11 +245,11 @@ __device__ __forceinline__ int4 ld_cluster_int4(uint32_t addr) {
     return v;
 }
 
-template <int BT, int kSplits>
+template <int BT, int kSplits, int XQ>
 __global__ void __launch_bounds__(NT, 1)
 linear_i8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_w,
                       const __grid_constant__ I8Args p) {
-    using S = RowsShape<BT>;
+    using S = RowsShape<BT, XQ>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     const uint32_t sb = (raw + 1023u) & ~1023u;
@@ -199,7 +259,7 @@ linear_i8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
     auto empty = [&](int s) { return bar0 + 8u * (S::STAGES + s); };
     auto acc_full = [&](int a) { return bar0 + 8u * (2 * S::STAGES + a); };
     auto acc_empty = [&](int a) { return bar0 + 8u * (2 * S::STAGES + 2 + a); };
-    const uint32_t drain = bar0 + 8u * (2 * S::STAGES + 4);
+    const uint32_t drain = bar0 + 8u * (2 * S::STAGES + 4), x_ready = drain + 8u;
     volatile uint32_t* s_tmem = reinterpret_cast<volatile uint32_t*>(smem + S::OFF_BAR + S::N_BARS * 8);
     volatile uint32_t* s_abort = s_tmem + 1;
 
@@ -214,6 +274,7 @@ linear_i8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
             mbar_init(acc_empty(a), 4);
         }
         mbar_init(drain, 1);
+        mbar_init(x_ready, 4);
         *s_abort = 0;
         fence_mbar_init();
     }
@@ -239,7 +300,6 @@ linear_i8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
     if (warp == 0) {
         // ---- TMA producer (one thread) ----
         if (lane == 0) {
-            prefetch_tmap(&tm_x);
             prefetch_tmap(&tm_w);
             const uint32_t total = (uint32_t)my_tiles * kb_n;
             const uint32_t pre = total < (uint32_t)S::STAGES ? total : S::STAGES;
@@ -248,10 +308,12 @@ linear_i8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
                 tma_load_2d(sb + (uint32_t)s * S::STAGE, &tm_w, kb * BK8, tile * p.tile_rows, full(s));
             };
             auto load_x = [&](uint32_t it, int s) {
+                if constexpr (XQ > 0) return;
                 const int kb = k_lo + (int)(it % kb_n);
                 tma_load_2d(sb + (uint32_t)s * S::STAGE + S::W_BYTES, &tm_x, kb * BK8, 0, full(s));
             };
             const uint32_t bytes = (uint32_t)(p.tile_rows * BK8 + S::X_BYTES);   // of a stage
+            if constexpr (XQ == 0) prefetch_tmap(&tm_x);
             if (!p.w_ready) grid_dependency_wait();
             for (uint32_t it = 0; it < pre; ++it) {
                 mbar_arrive_expect_tx(full(it), bytes);
@@ -286,6 +348,7 @@ linear_i8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
         constexpr uint32_t ID = idesc_i8(128, BT);
         uint32_t it = 0;
         bool ok = true;
+        if constexpr (XQ > 0) ok = mbar_wait_bounded(x_ready, 0);
         for (int ti = 0; ti < my_tiles && ok; ++ti) {
             const uint32_t a = ti & 1u;
             if (!mbar_wait_bounded(acc_empty(a), ((ti >> 1) & 1u) ^ 1u) || *s_abort) {
@@ -302,10 +365,10 @@ linear_i8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
                 }
                 tc_fence_after();
                 const uint32_t src = sb + (uint32_t)s * S::STAGE;
+                const uint32_t xsrc = XQ > 0 ? sb + S::OFF_XQ + kb * (BT * BK8) : src + S::W_BYTES;
 #pragma unroll
                 for (int k = 0; k < 4; ++k)   // 32 int8 of K each
-                    mma_i8_w(d, sdesc(src + k * 32, 16, 1024), sdesc(src + S::W_BYTES + k * 32, 16, 1024), ID,
-                             (kb | k) != 0);
+                    mma_i8_w(d, sdesc(src + k * 32, 16, 1024), sdesc(xsrc + k * 32, 16, 1024), ID, (kb | k) != 0);
                 mma_commit_w(empty(s));
             }
             if (!ok) break;
@@ -322,9 +385,25 @@ linear_i8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
         // ---- epilogue: this thread's channel, all tokens ----
         const int q = warp & 3;
         const int row = q * 32 + lane;
-        grid_dependency_wait();   // (the rows' scales)
+        grid_dependency_wait();   // (the rows, or their scales)
         float* xs = reinterpret_cast<float*>(smem + S::OFF_XS);
-        if ((int)threadIdx.x - 64 < BT) xs[threadIdx.x - 64] = (int)threadIdx.x - 64 < p.M ? p.x_scale[threadIdx.x - 64] : 0.0f;
+        if constexpr (XQ > 0) {
+            using Raw = RawShape<XQ>;
+            static_assert(BT == 16 && 8 + 4 * Raw::ROWS <= BT, "scales and scratch");
+            uint8_t* xq = smem + S::OFF_XQ;
+            const int t = (int)threadIdx.x - 64;
+            if (p.x_f32)
+                raw_rows_to_i8<float, Raw::ROWS, Raw::VECS>(static_cast<const float*>(p.x_raw), (int)p.M, p.K, k_lo, kb_n,
+                                                            xq, BT * BK8, xs, t);
+            else
+                raw_rows_to_i8<__nv_bfloat16, Raw::ROWS, Raw::VECS>(static_cast<const __nv_bfloat16*>(p.x_raw), (int)p.M,
+                                                                    p.K, k_lo, kb_n, xq, BT * BK8, xs, t);
+            fence_async_smem();   // (the MMA reads them)
+            __syncwarp();
+            if (lane == 0) arrive(x_ready);
+        } else if ((int)threadIdx.x - 64 < BT) {
+            xs[threadIdx.x - 64] = (int)threadIdx.x - 64 < p.M ? p.x_scale[threadIdx.x - 64] : 0.0f;
+        }
         asm volatile("bar.sync 1, 128;" ::: "memory");   // (the epilogue warps)
         bool ok = true;
         for (int ti = 0; ti < my_tiles; ++ti) {

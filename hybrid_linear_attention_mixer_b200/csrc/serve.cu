@@ -210,10 +210,10 @@ int pick_bn_i8(int64_t M, int N, int pairs) {
 
 constexpr int kMinTileRows = 96, kJoinCost = 250;
 
-template <int BT, int kSplits>
+template <int BT, int kSplits, int XQ>
 struct RowsForm {
-    using S = gdn::gemm::RowsShape<BT>;
-    static constexpr auto kernel = gdn::gemm::linear_i8_rows_kernel<BT, kSplits>;
+    using S = gdn::gemm::RowsShape<BT, XQ>;
+    static constexpr auto kernel = gdn::gemm::linear_i8_rows_kernel<BT, kSplits, XQ>;
     static int at_once() {   // (the runtime counts what the kernel is allowed)
         return allow_smem<kernel>(S::SMEM) == cudaSuccess ? resident_clusters<kernel>(kSplits, gdn::gemm::NT, S::SMEM) : 0;
     }
@@ -226,13 +226,15 @@ struct RowsForm {
     }
 };
 
+// Tile height and split of K: the fewest bytes (of 128) that one CTA loads, over the
+// clusters that run at once; a split (one tile per cluster) pays for its join.  Heights
+// below 128 even out the waves (64 rows x 64,000 outputs x 2560: 29.7 us, 31.7 with 128).
+// Sets a's tile height and count; returns log2 of the split.
 template <int BT>
-cudaError_t launch_i8_rows(const void* x, const void* w, gdn::gemm::I8Args a, cudaStream_t st) {
-    // Tile height and split of K: the fewest bytes (of 128) that one CTA loads, over the
-    // clusters that run at once; a split (one tile per cluster) pays for its join.  Heights
-    // below 128 even out the waves (64 rows x 64,000 outputs x 2560: 29.7 us, 31.7 with 128).
+int plan_i8_rows(gdn::gemm::I8Args& a) {
     const int kb = (a.K + gdn::gemm::BK8 - 1) / gdn::gemm::BK8;
-    const int at_once[4] = {sm_count(), RowsForm<BT, 2>::at_once(), RowsForm<BT, 4>::at_once(), RowsForm<BT, 8>::at_once()};
+    const int at_once[4] = {sm_count(), RowsForm<BT, 2, 0>::at_once(), RowsForm<BT, 4, 0>::at_once(),
+                            RowsForm<BT, 8, 0>::at_once()};
     int best = 0;
     int64_t best_cost = INT64_MAX;
     for (int i = 0; i < 4 && (1 << i) <= kb; ++i) {
@@ -250,14 +252,43 @@ cudaError_t launch_i8_rows(const void* x, const void* w, gdn::gemm::I8Args a, cu
             }
         }
     }
+    return best;
+}
+
+template <int BT, int XQ>
+cudaError_t launch_i8_rows_planned(const void* x, const void* w, const gdn::gemm::I8Args& a, int split, cudaStream_t st) {
     CUtensorMap tm_x, tm_w;
-    if (!i8_map(&tm_x, x, a.M, a.K, BT) || !i8_map(&tm_w, w, a.N, a.K, a.tile_rows)) return cudaErrorInvalidValue;
-    switch (best) {
-        case 0: return RowsForm<BT, 1>::launch(tm_x, tm_w, a, st);
-        case 1: return RowsForm<BT, 2>::launch(tm_x, tm_w, a, st);
-        case 2: return RowsForm<BT, 4>::launch(tm_x, tm_w, a, st);
-        default: return RowsForm<BT, 8>::launch(tm_x, tm_w, a, st);
+    if (!i8_map(&tm_w, w, a.N, a.K, a.tile_rows)) return cudaErrorInvalidValue;
+    if (XQ > 0) tm_x = tm_w;   // (not used)
+    else if (!i8_map(&tm_x, x, a.M, a.K, BT)) return cudaErrorInvalidValue;
+    switch (split) {
+        case 0: return RowsForm<BT, 1, XQ>::launch(tm_x, tm_w, a, st);
+        case 1: return RowsForm<BT, 2, XQ>::launch(tm_x, tm_w, a, st);
+        case 2: return RowsForm<BT, 4, XQ>::launch(tm_x, tm_w, a, st);
+        default: return RowsForm<BT, 8, XQ>::launch(tm_x, tm_w, a, st);
     }
+}
+
+template <int BT>
+cudaError_t launch_i8_rows(const void* x, const void* w, gdn::gemm::I8Args a, cudaStream_t st) {
+    const int split = plan_i8_rows<BT>(a);
+    return launch_i8_rows_planned<BT, 0>(x, w, a, split, st);
+}
+
+// One or two rows in bf16 or fp32, by one launch: true if the form takes them (the rows' 8-bit
+// k-blocks fit beside the ring).
+bool launch_i8_raw_rows(const void* w, gdn::gemm::I8Args a, cudaStream_t st, cudaError_t* e) {
+    const int kb = (a.K + gdn::gemm::BK8 - 1) / gdn::gemm::BK8;
+    if (a.M <= gdn::gemm::RawShape<24>::ROWS && kb <= 24) {
+        const int split = plan_i8_rows<16>(a);
+        *e = launch_i8_rows_planned<16, 24>(nullptr, w, a, split, st);
+    } else if (a.M <= gdn::gemm::RawShape<48>::ROWS && kb <= 48) {
+        const int split = plan_i8_rows<16>(a);
+        *e = launch_i8_rows_planned<16, 48>(nullptr, w, a, split, st);
+    } else {
+        return false;
+    }
+    return true;
 }
 
 // 8-bit rows, then their scales, in the workspace.
@@ -309,6 +340,11 @@ gdn_status run_linear_i8(const void* x, int32_t x_dtype, const float* x_scale, c
     if (quantize) {
         if (x_scale || !workspace || !aligned(workspace, 256)) return GDN_ERR_INVALID_ARG;
         if (workspace_bytes < ws_need) return GDN_ERR_WORKSPACE;
+        a.x_raw = x;
+        a.x_f32 = x_dtype == GDN_F32;
+        a.w_scale = w_scale;
+        cudaError_t e;
+        if (launch_i8_raw_rows(w, a, st, &e)) return cuda_status(e);
         int8_t* q = static_cast<int8_t*>(workspace);
         float* scale = reinterpret_cast<float*>(q + i8_scale_off(M, K));
         const gdn_status s = run_quantize(x, x_dtype, M, K, q, scale, st);

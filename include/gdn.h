@@ -390,8 +390,9 @@ gdn_status gdn_quantize_rows(const void* x, int32_t x_dtype, int64_t rows, int32
  * The sum is exact (int32, on the tensor cores); it is converted to fp32, multiplied
  * by the two scales' fp32 product and rounded to out_dtype.
  *   x  [M][K]: GDN_I8 with its scales x_scale [M]; or GDN_BF16 / GDN_F32 with
- *      x_scale NULL: the call makes the 8-bit rows itself (gdn_quantize_rows) in
- *      its workspace of gdn_linear_i8_workspace_size bytes, 256-byte aligned
+ *      x_scale NULL: the call makes the 8-bit rows itself (those of
+ *      gdn_quantize_rows, bit for bit) and takes a workspace for them, of
+ *      gdn_linear_i8_workspace_size bytes, 256-byte aligned
  *   w  [N][K] int8, w_scale [N] float32
  *   K a multiple of 16, at most 131056 (128 * 128 * K must fit in 31 bits); N a
  *   multiple of 8 (else GDN_ERR_UNSUPPORTED).  The columns of y are split over segs

@@ -232,7 +232,10 @@ def test_linear_i8(M, N, K, out):
     check_linear(torch.cat(outs, 1), x, xs, w, ws, out)
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 16480, 2560), (3, 80, 48), (16, 520, 2560), (65, 264, 6144), (200, 520, 2576)])
+@pytest.mark.parametrize("M,N,K", [(1, 16480, 2560), (3, 80, 48), (16, 520, 2560), (65, 264, 6144), (200, 520, 2576),
+                                   (8, 2560, 6144), (5, 20000, 6144), (2, 72, 16), (7, 1000, 2576), (8, 40, 12304),
+                                   (1, 30000, 7000 // 16 * 16), (4, 24, 131056), (9, 2560, 2560),
+                                   (1, 2560, 6144), (2, 2560, 2560), (1, 264, 144), (2, 5000, 2000), (1, 30000, 5104)])
 @pytest.mark.parametrize("x_dt", ["bf16", "f32"])
 def test_linear_i8_makes_the_rows(M, N, K, x_dt):
     """From bf16 / fp32 rows: bit for bit what gdn_quantize_rows and the 8-bit call give."""
@@ -242,6 +245,19 @@ def test_linear_i8_makes_the_rows(M, N, K, x_dt):
     y8 = gdn.linear_i8(q, w, ws, x_scale=xs, out_dtype=torch.float32)[0]
     assert torch.equal(y, y8)
     check_linear(y, x, None, w, ws, "f32")
+
+
+def test_linear_i8_few_rows_not_finite_or_zero():
+    """What gdn_quantize_rows does with such rows, where the product makes them 8-bit itself."""
+    M, N, K = 6, 264, 2560
+    x, _, w, ws = i8_case(M, N, K, 5, "bf16")
+    x[1], x[2, 7], x[3, 2559], x[4] = 0, float("inf"), float("nan"), x[4] * 1e38
+    for step in (1, 2, M):
+        y = torch.cat([gdn.linear_i8(x[i:i + step], w, ws, out_dtype=torch.float32)[0] for i in range(0, M, step)])
+        q, xs = gdn.quantize_rows(x)
+        y8 = gdn.linear_i8(q, w, ws, x_scale=xs, out_dtype=torch.float32)[0]
+        assert torch.equal(torch.nan_to_num(y, 7.0), torch.nan_to_num(y8, 7.0)) and torch.equal(torch.isnan(y), torch.isnan(y8))
+        assert torch.isnan(y[2:4]).all() and not y[1].any() and torch.isfinite(y[[0, 1, 5]]).all()
 
 
 def test_linear_i8_weights_written_just_before():
