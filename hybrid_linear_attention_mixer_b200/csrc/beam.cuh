@@ -626,11 +626,14 @@ __global__ void __launch_bounds__(MT) merge_kernel(const __grid_constant__ Args 
     grid_dependency_trigger();
     grid_dependency_wait();
     const uint64_t* keys = p.cand + row0 * p.slices * p.n;
-    if (p.keys_in_smem) {   // (of rows that left none too: whatever is there is not used)
-        uint64_t* mine = reinterpret_cast<uint64_t*>(cand + merge_cap(p.n));
-        for (int i = tid; i < lists * p.n; i += MT) mine[i] = keys[i];
-        keys = mine;
-    }
+    // The group's keys, on their way while the rows' sums are formed (of rows that left none
+    // too: whatever is there is not used).
+    constexpr int kAhead = 4;
+    const int n_keys = p.keys_in_smem ? lists * p.n : 0;
+    uint64_t ahead[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+        if (tid + i * MT < n_keys) ahead[i] = keys[tid + i * MT];
 
     for (int w = warp; w < p.W; w += MT / 32) {
         const int64_t row = row0 + w;
@@ -679,6 +682,14 @@ __global__ void __launch_bounds__(MT) merge_kernel(const __grid_constant__ Args 
             offset[w] = off;
             kind[w] = !isfinite(off) ? 0 : fin ? 2 : 1;
         }
+    }
+    if (p.keys_in_smem) {
+        uint64_t* mine = reinterpret_cast<uint64_t*>(cand + merge_cap(p.n));
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (tid + i * MT < n_keys) mine[tid + i * MT] = ahead[i];
+        for (int i = tid + kAhead * MT; i < n_keys; i += MT) mine[i] = keys[i];
+        keys = mine;
     }
     __syncthreads();
     // Entry e of list l, which is beam w's.  A finished beam's one entry is the first of its
