@@ -293,9 +293,11 @@ linear_i8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
     const int kb_all = (p.K + BK8 - 1) / BK8;
     const int k_lo = (int)((int64_t)kb_all * rank / kSplits);
     const int kb_n = (int)((int64_t)kb_all * (rank + 1) / kSplits) - k_lo;
-    const int tiles = p.n_blocks;
+    const int tiles = p.n_blocks * p.m_blocks;   // (with more than one block of tokens, one tile a CTA)
     const int first = blockIdx.x / kSplits, step = gridDim.x / kSplits;
     const int my_tiles = first < tiles ? (tiles - first + step - 1) / step : 0;
+    const int m0 = first / p.n_blocks * BT, n_tile0 = first % p.n_blocks;   // first token, first tile of channels
+    const int m_here = (int)min((int64_t)BT, p.M - m0);                     // tokens of the block
 
     if (warp == 0) {
         // ---- TMA producer (one thread) ----
@@ -304,13 +306,13 @@ linear_i8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
             const uint32_t total = (uint32_t)my_tiles * kb_n;
             const uint32_t pre = total < (uint32_t)S::STAGES ? total : S::STAGES;
             auto load_w = [&](uint32_t it, int s) {
-                const int tile = first + (int)(it / kb_n) * step, kb = k_lo + (int)(it % kb_n);
+                const int tile = n_tile0 + (int)(it / kb_n) * step, kb = k_lo + (int)(it % kb_n);
                 tma_load_2d(sb + (uint32_t)s * S::STAGE, &tm_w, kb * BK8, tile * p.tile_rows, full(s));
             };
             auto load_x = [&](uint32_t it, int s) {
                 if constexpr (XQ > 0) return;
                 const int kb = k_lo + (int)(it % kb_n);
-                tma_load_2d(sb + (uint32_t)s * S::STAGE + S::W_BYTES, &tm_x, kb * BK8, 0, full(s));
+                tma_load_2d(sb + (uint32_t)s * S::STAGE + S::W_BYTES, &tm_x, kb * BK8, m0, full(s));
             };
             const uint32_t bytes = (uint32_t)(p.tile_rows * BK8 + S::X_BYTES);   // of a stage
             if constexpr (XQ == 0) prefetch_tmap(&tm_x);
@@ -402,13 +404,13 @@ linear_i8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
             __syncwarp();
             if (lane == 0) arrive(x_ready);
         } else if ((int)threadIdx.x - 64 < BT) {
-            xs[threadIdx.x - 64] = (int)threadIdx.x - 64 < p.M ? p.x_scale[threadIdx.x - 64] : 0.0f;
+            xs[threadIdx.x - 64] = (int)threadIdx.x - 64 < m_here ? p.x_scale[m0 + threadIdx.x - 64] : 0.0f;
         }
         asm volatile("bar.sync 1, 128;" ::: "memory");   // (the epilogue warps)
         bool ok = true;
         for (int ti = 0; ti < my_tiles; ++ti) {
             const uint32_t a = ti & 1u;
-            const int n = row < p.tile_rows ? (first + ti * step) * p.tile_rows + row : p.N;
+            const int n = row < p.tile_rows ? (n_tile0 + ti * step) * p.tile_rows + row : p.N;
             const float ws = n < p.N ? p.w_scale[n] : 0.0f;
             const Seg& sg = segment_of(p, n);
             if (!mbar_wait_bounded(acc_full(a), (ti >> 1) & 1u) || *s_abort) {
@@ -427,8 +429,8 @@ linear_i8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
                         asm volatile("st.shared.b32 [%0], %1;" ::"r"(sb + ((c * 16 + i) * 128 + row) * 4), "r"(r[i])
                                      : "memory");
                 } else if (n < p.N) {
-                    const int64_t at = (int64_t)(c * 16) * sg.width + (n - sg.n0);
-                    const int left = (int)p.M - c * 16;
+                    const int64_t at = (int64_t)(m0 + c * 16) * sg.width + (n - sg.n0);
+                    const int left = m_here - c * 16;
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         if (i >= left) break;
@@ -452,13 +454,13 @@ linear_i8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
         // One tile per cluster.  CTA m % kSplits adds up token m, a warp to a token and a
         // lane to four channels.
         cluster_sync();
-        const int n = lane * 4 < p.tile_rows ? first * p.tile_rows + lane * 4 : p.N;
+        const int n = lane * 4 < p.tile_rows ? n_tile0 * p.tile_rows + lane * 4 : p.N;
         if (warp >= 2 && !*s_abort && my_tiles > 0 && n < p.N) {
             const float* xs = reinterpret_cast<const float*>(smem + S::OFF_XS);
             const Seg& sg = segment_of(p, n);
             const float4 ws = __ldg(reinterpret_cast<const float4*>(p.w_scale + n));
 #pragma unroll 2
-            for (int m = rank + (warp - 2) * kSplits; m < p.M; m += 4 * kSplits) {
+            for (int m = rank + (warp - 2) * kSplits; m < m_here; m += 4 * kSplits) {
                 int4 v[kSplits];
 #pragma unroll
                 for (int r = 0; r < kSplits; ++r) v[r] = ld_cluster_int4(map_to_rank(sb + (m * 128 + lane * 4) * 4, r));
@@ -472,7 +474,7 @@ linear_i8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
                 const float f = xs[m];
                 const float4 y = make_float4((float)v[0].x * (f * ws.x), (float)v[0].y * (f * ws.y),
                                              (float)v[0].z * (f * ws.z), (float)v[0].w * (f * ws.w));
-                const int64_t at = (int64_t)m * sg.width + (n - sg.n0);
+                const int64_t at = (int64_t)(m0 + m) * sg.width + (n - sg.n0);
                 if (p.out_f32) {
                     *reinterpret_cast<float4*>(reinterpret_cast<float*>(sg.dst) + at) = y;
                 } else {

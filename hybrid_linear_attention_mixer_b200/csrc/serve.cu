@@ -192,7 +192,8 @@ cudaError_t launch_i8_pair(const void* x, const void* w, gdn::gemm::I8Args a, cu
 // waves x (operand bytes of a k-block, 128 x (256 + BN) of a pair).  The bytes from L2 bound
 // a k-block, not the MMA, which takes half the bf16 form's time: 4096 x 16480 x 2560 at 256
 // (15 waves) 127 us, at 224 (16) 131, at 192 (19) 142; the bf16 form's rule took 224.
-int pick_bn_i8(int64_t M, int N, int pairs) {
+// *cost: those bytes of one CTA in units of 128 times K's k-blocks, as for the other form.
+int pick_bn_i8(int64_t M, int N, int pairs, int64_t* cost_out) {
     static const int cand[] = {256, 224, 192, 160, 128};
     const int64_t mp = (M + 2 * gdn::gemm::BM - 1) / (2 * gdn::gemm::BM);
     int best = 256;
@@ -205,10 +206,12 @@ int pick_bn_i8(int64_t M, int N, int pairs) {
             best_cost = cost;
         }
     }
+    *cost_out = best_cost / 2;
     return best;
 }
 
-constexpr int kMinTileRows = 96, kJoinCost = 250;
+constexpr int kMinTileRows = 96, kJoinCost = 250, kBlocksCost = 950;
+constexpr int64_t kMaxRowsM = 148 * 128;   // no more blocks of tokens than SMs
 
 template <int BT, int kSplits, int XQ>
 struct RowsForm {
@@ -221,7 +224,7 @@ struct RowsForm {
                               cudaStream_t st) {
         const cudaError_t e = allow_smem<kernel>(S::SMEM);
         if (e != cudaSuccess) return e;
-        const int grid = kSplits > 1 ? a.n_blocks * kSplits : std::min(a.n_blocks, sm_count());
+        const int tiles = a.n_blocks * a.m_blocks, grid = kSplits > 1 ? tiles * kSplits : std::min(tiles, sm_count());
         return Launch((unsigned)grid, gdn::gemm::NT, S::SMEM, st).cluster(kSplits)(kernel, tm_x, tm_w, a);
     }
 };
@@ -229,29 +232,34 @@ struct RowsForm {
 // Tile height and split of K: the fewest bytes (of 128) that one CTA loads, over the
 // clusters that run at once; a split (one tile per cluster) pays for its join.  Heights
 // below 128 even out the waves (64 rows x 64,000 outputs x 2560: 29.7 us, 31.7 with 128).
-// Sets a's tile height and count; returns log2 of the split.
+// Sets a's tile height and counts; returns log2 of the split and the cost, or -1 where the
+// tokens take several blocks and their tiles do not all run at once.
 template <int BT>
-int plan_i8_rows(gdn::gemm::I8Args& a) {
+int plan_i8_rows(gdn::gemm::I8Args& a, int64_t* cost_out = nullptr) {
+    const int64_t m_blocks = (a.M + BT - 1) / BT;
     const int kb = (a.K + gdn::gemm::BK8 - 1) / gdn::gemm::BK8;
     const int at_once[4] = {sm_count(), RowsForm<BT, 2, 0>::at_once(), RowsForm<BT, 4, 0>::at_once(),
                             RowsForm<BT, 8, 0>::at_once()};
-    int best = 0;
+    int best = -1;
     int64_t best_cost = INT64_MAX;
     for (int i = 0; i < 4 && (1 << i) <= kb; ++i) {
         if (at_once[i] <= 0) break;
         for (int rows = 128; rows >= kMinTileRows; rows -= 8) {
-            const int tiles = (a.N + rows - 1) / rows;
-            if (i > 0 && tiles > at_once[i]) break;
-            const int64_t cost = (int64_t)((tiles + at_once[i] - 1) / at_once[i]) * (rows + BT) * ((kb + (1 << i) - 1) >> i) +
+            const int n_blocks = (a.N + rows - 1) / rows;
+            const int64_t tiles = n_blocks * m_blocks;
+            if ((i > 0 || m_blocks > 1) && tiles > at_once[i]) break;
+            const int64_t cost = (tiles + at_once[i] - 1) / at_once[i] * (rows + BT) * ((kb + (1 << i) - 1) >> i) +
                                  (i > 0 ? kJoinCost : 0);
             if (cost < best_cost) {
                 best_cost = cost;
                 best = i;
                 a.tile_rows = rows;
-                a.n_blocks = tiles;
+                a.n_blocks = n_blocks;
+                a.m_blocks = (int)m_blocks;
             }
         }
     }
+    if (cost_out) *cost_out = best_cost;
     return best;
 }
 
@@ -363,12 +371,24 @@ gdn_status run_linear_i8(const void* x, int32_t x_dtype, const float* x_scale, c
     else if (M <= 64) e = launch_i8_rows<64>(x, w, a, st);
     else if (M <= 128) e = launch_i8_rows<128>(x, w, a, st);
     else {
-        switch (pick_bn_i8(M, N, std::max(1, sm_count() / 2))) {
-            case 256: e = launch_i8_pair<256>(x, w, a, st); break;
-            case 224: e = launch_i8_pair<224>(x, w, a, st); break;
-            case 192: e = launch_i8_pair<192>(x, w, a, st); break;
-            case 160: e = launch_i8_pair<160>(x, w, a, st); break;
-            default: e = launch_i8_pair<128>(x, w, a, st); break;
+        // Several blocks of 128 tokens in the form for few rows where its tiles, with K split,
+        // all run at once and load fewer bytes a CTA than pair tiles do by more than its longer
+        // epilogue: 252 x 1728 x 3616 7.8 us, 11.1 in pair tiles; 256 x 2560 x 6144 12.4 and
+        // 16.0; but 3841 x 152 x 1504 7.8 and 7.2, 1000 x 520 x 1040 7.5 and 6.7.
+        int64_t rows_cost = 0, pair_cost = 0;
+        gdn::gemm::I8Args r = a;
+        const int bn = pick_bn_i8(M, N, std::max(1, sm_count() / 2), &pair_cost);
+        const int split = M <= kMaxRowsM ? plan_i8_rows<128>(r, &rows_cost) : -1;
+        if (split >= 0 && rows_cost + kBlocksCost < pair_cost * ((K + gdn::gemm::BK8 - 1) / gdn::gemm::BK8)) {
+            e = launch_i8_rows_planned<128, 0>(x, w, r, split, st);
+        } else {
+            switch (bn) {
+                case 256: e = launch_i8_pair<256>(x, w, a, st); break;
+                case 224: e = launch_i8_pair<224>(x, w, a, st); break;
+                case 192: e = launch_i8_pair<192>(x, w, a, st); break;
+                case 160: e = launch_i8_pair<160>(x, w, a, st); break;
+                default: e = launch_i8_pair<128>(x, w, a, st); break;
+            }
         }
     }
     return cuda_status(e);

@@ -217,7 +217,10 @@ def check_linear(y, x, xs, w, ws, out, rows=None, cols=None):
 
 I8_SHAPES = [(1, 8, 16), (1, 16480, 2560), (5, 200, 144), (16, 136, 6144), (17, 1000, 272), (33, 2560, 6144),
              (64, 5000, 400), (100, 264, 2576), (128, 384, 160), (129, 264, 144), (257, 2312, 2560), (1000, 520, 1040),
-             (300, 4040, 128), (1000, 2888, 64), (700, 3464, 32)]
+             (300, 4040, 128), (1000, 2888, 64), (700, 3464, 32),
+             # every pair tile width (160, 192, 224, 256, 128 with 74 pairs), then blocks of 128 tokens with K split
+             (1000, 2600, 272), (1000, 3000, 272), (1000, 3496, 272), (1000, 4040, 272), (2500, 896, 272),
+             (252, 1728, 3616), (130, 160, 6144), (513, 400, 2064), (900, 136, 1040), (129, 8, 16)]
 
 
 @pytest.mark.parametrize("M,N,K", I8_SHAPES)
