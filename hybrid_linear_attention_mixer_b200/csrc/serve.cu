@@ -309,7 +309,8 @@ gdn_status run_linear_i8(const void* x, int32_t x_dtype, const float* x_scale, c
     if ((x_dtype != GDN_I8 && !float_dtype(x_dtype)) || !float_dtype(out_dtype)) return GDN_ERR_INVALID_ARG;
     if (n_segs > GDN_LINEAR_MAX_SEGMENTS) return GDN_ERR_UNSUPPORTED;
     if (N % 8 != 0 || K % 16 != 0 || K > 131056) return GDN_ERR_UNSUPPORTED;
-    if (M > 0x7fffffffLL - 256) return GDN_ERR_UNSUPPORTED;   // row coordinates are int32
+    // Row coordinates are int32, the end of a tile past the last row too (tiles have up to 256).
+    if (M > 0x7fffffffLL - 256 || N > 0x7fffffff - 256) return GDN_ERR_UNSUPPORTED;
     gdn::gemm::I8Args a = {};
     a.M = M;
     a.N = N;

@@ -395,8 +395,9 @@ gdn_status gdn_quantize_rows(const void* x, int32_t x_dtype, int64_t rows, int32
  *      gdn_linear_i8_workspace_size bytes, 256-byte aligned
  *   w  [N][K] int8, w_scale [N] float32
  *   K a multiple of 16, at most 131056 (128 * 128 * K must fit in 31 bits); N a
- *   multiple of 8 (else GDN_ERR_UNSUPPORTED).  The columns of y are split over segs
- *   as in gdn_linear; dst holds out_dtype (GDN_BF16 or GDN_F32).
+ *   multiple of 8; M and N at most 2^31 - 257 (else GDN_ERR_UNSUPPORTED).  The
+ *   columns of y are split over segs as in gdn_linear; dst holds out_dtype
+ *   (GDN_BF16 or GDN_F32).
  * x, w, w_scale and the destinations are 16-byte aligned.  The scales may be
  * anything, NaN and infinities included.  Nothing written (the destinations, the
  * workspace) may overlap anything else.  M == 0 is a no-op.

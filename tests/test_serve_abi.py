@@ -129,6 +129,16 @@ def test_linear_i8_argument_errors(lib):
         assert call(dt=BF16, xs=0, wk=wk, wkb=size) == INVALID
 
 
+def test_linear_i8_most_outputs(lib):
+    """Output numbers, and a tile past the last of them, are 32 bits (x is null: the sizes
+    are answered first)."""
+    def call(N, M=4):
+        return lib.gdn_linear_i8(None, I8, P(MB), P(MB), P(MB), M, N, 16, BF16, _segs(N), 1, None, 0, None)
+    for M in (0, 1, 4, 4096):
+        assert call(2 ** 31 - 8, M) == UNSUPPORTED and call(2 ** 31 - 256, M) == UNSUPPORTED
+    assert call(2 ** 31 - 264) == INVALID and call(2 ** 31 - 264, 0) == OK
+
+
 def test_projections_i8_argument_errors(lib):
     c = gdn.Config().c()
     inp = lambda cfg, T, D: lib.gdn_in_proj_i8(ctypes.byref(cfg), P(MB), I8, P(MB), P(MB), P(MB), T, D, *[P(MB)] * 6, None, 0, None)
