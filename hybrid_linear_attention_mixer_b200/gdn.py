@@ -727,7 +727,10 @@ class ReorderPlan:
     def __init__(self, states, n_groups: int, n_beams: int):
         if not 0 < len(states) <= REORDER_MAX_BUFFERS:
             raise ValueError("1..%d states" % REORDER_MAX_BUFFERS)
-        self.states, self.n_groups, self.n_beams = list(states), int(n_groups), int(n_beams)
+        # (aliases: the memory behind the addresses stays while the plan does, even where the
+        # caller points a tensor at other memory)
+        self.states = [t.detach() for t in states]
+        self.n_groups, self.n_beams = int(n_groups), int(n_beams)
         self.device = _index_of(states[0], "states[0]")
         self.buffers = (_CStateBuffer * len(states))()
         for i, t in enumerate(self.states):
@@ -748,7 +751,7 @@ class ReorderPlan:
 def reorder_plan(states, n_groups: int, n_beams: int) -> ReorderPlan:
     """Checks the states (tensors [n_groups * n_beams, ...], each sequence's part
     contiguous) once, for ``reorder_states`` calls that move them again and again.  The
-    plan keeps the tensors."""
+    plan keeps their memory; a tensor that is pointed at other memory needs a new plan."""
     return ReorderPlan(states, n_groups, n_beams)
 
 

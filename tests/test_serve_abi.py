@@ -203,6 +203,21 @@ def test_reorder_argument_errors(lib):
     assert call([good], par=16 * MB + 64) == INVALID
 
 
+def test_reorder_plan_keeps_its_memory(monkeypatch):
+    """A plan's addresses stay those of memory that it keeps, whatever its tensors are
+    pointed at afterwards."""
+    monkeypatch.setattr(gdn, "_index_of", lambda t, name: t.get_device())
+    states = [torch.zeros(4, 8), torch.zeros(4, 16, requires_grad=True)]
+    plan = gdn.reorder_plan(states, 2, 2)
+    old = [t.data_ptr() for t in states]
+    states[0].data = torch.ones(4, 8)
+    with torch.no_grad():
+        states[1].set_(torch.ones(4, 16))
+    assert [b.base for b in plan.buffers] == old
+    assert [t.data_ptr() for t in plan.states] == old
+    assert all(int(torch.count_nonzero(t)) == 0 for t in plan.states)
+
+
 def test_status_string_of_the_index_check():
     assert gdn.status_string(8) not in {gdn.status_string(s) for s in range(8)} | {"unknown status"}
 
