@@ -158,17 +158,24 @@ def status_string(s: int) -> str:
 
 
 class _Fields:
-    """A dataclass whose C struct is made once and again after a field is set."""
+    """A dataclass whose C struct is kept for its next calls while the fields stay as they
+    are.  The struct is no part of the object's state: copies and pickles carry the fields."""
+    __slots__ = ("_made",)
 
-    def __setattr__(self, name, value):
-        self.__dict__.pop("_made", None)
-        object.__setattr__(self, name, value)
+    def __getstate__(self):
+        return self.__dict__.copy()
 
     def ref(self):
         """A pointer to the C struct, for a call."""
-        made = self.__dict__.get("_made")
-        if made is None:
-            made = self.__dict__["_made"] = ctypes.byref(self.c())
+        now = [*self.__dict__.values()]
+        try:
+            was, made = self._made
+            if was == now:
+                return made
+        except AttributeError:   # the first call
+            pass
+        made = ctypes.byref(self.c())
+        self._made = now, made
         return made
 
 

@@ -1,6 +1,9 @@
 """The operators around the mixer: their host-side argument checks, which answer without a
 GPU, and the references they are tested against (CPU only)."""
+import copy
 import ctypes
+import dataclasses
+import pickle
 
 import numpy as np
 import pytest
@@ -201,6 +204,25 @@ def test_reorder_argument_errors(lib):
     assert call([(16 * MB + 48, 64, 128), (16 * MB, 64, 128)]) == INVALID
     assert call([(16 * MB, 64, 128), (16 * MB + 64, 16, 256)]) == INVALID    # different strides, same span
     assert call([good], par=16 * MB + 64) == INVALID
+
+
+@pytest.mark.parametrize("make", [gdn.Config, gdn.NormConfig])
+def test_used_configs_copy_pickle_and_follow_their_fields(make):
+    """A configuration that calls have been made with is copied, pickled and taken apart like
+    a new one, and its next call has the values that its fields have then."""
+    cfg, field = make(), "d_v" if make is gdn.Config else "dim"
+    struct = gdn._CConfig if make is gdn.Config else gdn._CNormConfig
+    seen = lambda c: getattr(ctypes.cast(c.ref(), ctypes.POINTER(struct)).contents, field)
+    first = seen(cfg)
+    setattr(cfg, field, 64)
+    assert first != 64 and seen(cfg) == 64
+    for twin in (copy.copy(cfg), copy.deepcopy(cfg), pickle.loads(pickle.dumps(cfg)), make(**vars(cfg)),
+                 dataclasses.replace(cfg)):
+        assert twin == cfg and vars(twin) == vars(cfg) and seen(twin) == 64
+        setattr(twin, field, 32)
+        assert seen(twin) == 32 and seen(cfg) == 64
+    vars(cfg).update({field: 128})
+    assert seen(cfg) == 128
 
 
 def test_reorder_plan_keeps_its_memory(monkeypatch):
