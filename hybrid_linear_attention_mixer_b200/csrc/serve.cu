@@ -428,7 +428,14 @@ gdn_status beam_layout(int32_t n_groups, int32_t n_beams, int32_t vocab, int32_t
     const int64_t lists = (int64_t)n_groups * n_beams * L->slices;
     if (lists > 0x7fffffffLL) return GDN_ERR_UNSUPPORTED;   // (their numbers are 32 bits)
     L->cand_off = align_up((size_t)lists * sizeof(gdn::beam::Stat), 256);
-    L->total = L->cand_off + align_up((size_t)lists * n_out * sizeof(uint64_t), 256);
+    // The workspace asked for is that of the most lists that this many rows or fewer, of this
+    // length or shorter, make (there are fewer of them where more rows take longer slices), so
+    // that one for the largest call serves every smaller one: slices of `each` tiles are fewer
+    // than kBeamWarps in all (each > rows tiles / kBeamWarps) and each >= kBeamTiles, but a
+    // row has one slice at least, and one for every TILES tiles.
+    const int64_t most = std::max(std::min<int64_t>(kBeamWarps, rows * L->tiles / kBeamTiles),
+                                  rows * ((L->tiles + gdn::beam::TILES - 1) / gdn::beam::TILES));
+    L->total = align_up((size_t)most * sizeof(gdn::beam::Stat), 256) + align_up((size_t)most * n_out * sizeof(uint64_t), 256);
     return GDN_OK;
 }
 

@@ -446,7 +446,8 @@ gdn_status gdn_out_proj_i8(const gdn_config* cfg, const void* o, int32_t x_dtype
  * 1 <= n_beams <= 32, 1 <= n_out <= 64, 1 <= vocab <= 2^20 (larger:
  * GDN_ERR_UNSUPPORTED); 0 <= pad_token < vocab; n_groups == 0 is a no-op.  workspace
  * of gdn_beam_workspace_size bytes (0: unsupported sizes), 256-byte aligned, its
- * contents need not be initialised.
+ * contents need not be initialised.  The size grows with each of n_groups, n_beams,
+ * vocab and n_out, so the workspace of a call serves every call with none of them larger.
  */
 size_t gdn_beam_workspace_size(int32_t n_groups, int32_t n_beams, int32_t vocab, int32_t n_out,
                                int32_t logits_dtype);

@@ -183,6 +183,31 @@ def test_beam_argument_errors(lib):
     assert call(ws=16 * MB) == INVALID and call(fin=33 * MB) == INVALID
 
 
+@pytest.mark.parametrize("dt,size", [(torch.bfloat16, 2), (torch.float32, 4)])
+def test_beam_workspace_of_a_call_serves_smaller_ones(lib, dt, size):
+    """No size that a request loses may make its step need more: batches that shrink, beams
+    that are dropped, fewer results, a shorter vocabulary."""
+    need = lambda G, W, V, n: gdn.beam_workspace_size(G, W, V, n, dt)
+    for W, V, n in ((4, 128256, 4), (5, 32003, 10), (1, 1000, 1), (8, 248320, 16), (32, 1 << 20, 64), (3, 50001, 33), (16, 9000, 20)):
+        sizes = [need(G, W, V, n) for G in range(0, 1400)]
+        assert all(a <= b for a, b in zip(sizes, sizes[1:])), (W, V, n)
+    for G, V, n in ((1, 248320, 4), (19, 128256, 64), (300, 1 << 20, 7)):
+        sizes = [need(G, W, V, n) for W in range(1, 33)]
+        assert all(a <= b for a, b in zip(sizes, sizes[1:])), (G, V, n)
+    for G, W, V in ((1, 4, 248320), (64, 8, 32003), (1000, 3, 700)):
+        sizes = [need(G, W, V, n) for n in range(1, 65)]
+        assert all(a <= b for a, b in zip(sizes, sizes[1:])), (G, W, V)
+    for G, W, n in ((1, 1, 1), (3, 5, 9), (70, 4, 64)):
+        sizes = [need(G, W, V, n) for V in range(1, 1 << 20, 997)]
+        assert all(a <= b for a, b in zip(sizes, sizes[1:])), (G, W, n)
+    # every candidate list of any layout that the call can take fits (16 bytes of sums and n keys each)
+    for G, W, V, n in ((18, 4, 128256, 4), (30, 5, 32003, 10), (1, 32, 1 << 20, 64), (2, 1, 30, 64), (500, 9, 70000, 2)):
+        tiles, rows = -(-V * size // 2048), G * W
+        each = min(max(rows * tiles // (148 * 32) + 1, 2, (n + 15) // 16), 32)
+        slices = min(max(tiles // each, 1, -(-tiles // 32)), 4096 // W)
+        assert need(G, W, V, n) >= rows * slices * (16 + 8 * n)
+
+
 def test_reorder_argument_errors(lib):
     def call(bufs, G=2, W=3, par=MB, n=None):
         arr = (gdn._CStateBuffer * max(1, len(bufs)))(*[gdn._CStateBuffer(*b) for b in bufs])
