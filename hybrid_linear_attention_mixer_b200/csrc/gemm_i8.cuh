@@ -347,6 +347,8 @@ linear_i8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
         }
     } else if (warp == 1) {
         // ---- MMA issuer (converged warp, elected lane issues) ----
+        // (the limits of the waits below are for this kernel's own work, not for the kernels before it)
+        grid_dependency_wait();
         constexpr uint32_t ID = idesc_i8(128, BT);
         uint32_t it = 0;
         bool ok = true;

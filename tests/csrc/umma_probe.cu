@@ -12,7 +12,8 @@
 // It also holds a test of the bounded wait: an mbarrier wait that nothing
 // completes gives up after its limit, records its code in the error word, and
 // the kernel returns; the host side maps the word to a status (the same
-// device.cuh code as the library's kernels and gdn_check_device_error).
+// device.cuh code as the library's kernels and gdn_check_device_error).  And a kernel
+// that lets the next one on its stream start at once and runs on for a given time.
 #include "../../hybrid_linear_attention_mixer_b200/csrc/device.cuh"
 
 using namespace gdn;
@@ -121,7 +122,20 @@ __global__ void __launch_bounds__(32, 1) wait_timeout_kernel(unsigned long long 
         *gave_up = done ? 0 : 1;
     }
 }
+// (ends after so many turns too, whatever the clock says)
+__global__ void __launch_bounds__(32, 1) run_on_kernel(unsigned long long ns) {
+    grid_dependency_trigger();
+    const unsigned long long t0 = global_ns();
+    for (int i = 0; i < 5000000 && global_ns() - t0 < ns; ++i) __nanosleep(1000);
+}
 }  // namespace
+
+// Launches the kernel above on `stream`, for ns nanoseconds (5 s at most).
+extern "C" int probe_run_on(unsigned long long ns, void* stream) {
+    if (ns > 5000000000ull) return 1;
+    run_on_kernel<<<1, 32, 0, static_cast<cudaStream_t>(stream)>>>(ns);
+    return cudaGetLastError() == cudaSuccess ? 0 : 2;
+}
 
 // Runs the wait above on `stream` and returns the status the error word maps to
 // (read and cleared), with the kernel's duration in *ms and its outcome in

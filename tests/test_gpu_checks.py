@@ -130,3 +130,28 @@ def test_conv_output_beyond_fp16_is_reported_and_nothing_is_written(segments, ro
     acts["q"] = inputs.f32_to_bf16_bits(inputs.bf16_bits_to_f32(c.acts["q"]) * 1.0e4)
     s, _, _ = _prefill_raw(c, cu, acts=acts, segments=segments)
     assert s == 0, gdn.status_string(s)
+
+
+# ---------------------------------------------------------------------------
+# Time that a kernel spends behind another one is not time that it waits for itself
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("M,N,K,x_dt", [(1, 16480, 2560, torch.bfloat16), (16, 2560, 6144, torch.int8),
+                                        (64, 20000, 400, torch.int8), (300, 16480, 272, torch.int8)])
+def test_products_behind_a_kernel_that_lets_them_start_and_runs_on(M, N, K, x_dt):
+    """A kernel ahead on the stream lets its successors start and then takes longer than a
+    bounded wait's limit (2 s): the product behind it reports nothing and is right."""
+    lib = _probe()
+    lib.probe_run_on.argtypes = [ctypes.c_ulonglong, ctypes.c_void_p]
+    g = torch.Generator(device=DEV).manual_seed(M)
+    i8 = lambda *s: torch.randint(-127, 128, s, generator=g, device=DEV, dtype=torch.int8)
+    w, ws = i8(N, K), torch.rand(N, generator=g, device=DEV)
+    x = i8(M, K) if x_dt == torch.int8 else torch.randn((M, K), generator=g, device=DEV).to(x_dt)
+    kw = {"x_scale": torch.rand(M, generator=g, device=DEV)} if x_dt == torch.int8 else {}
+    ref = gdn.linear_i8(x, w, ws, **kw)[0]
+    out = torch.zeros_like(ref)
+    work = torch.empty(gdn.linear_i8_workspace_size(M, K), dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    assert lib.probe_run_on(2_300_000_000, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == 0
+    gdn.linear_i8(x, w, ws, outs=[out], workspace=work, **kw)
+    gdn.check_device_error()
+    assert torch.equal(out, ref)
