@@ -167,9 +167,10 @@ struct Vec<float> {
     }
 };
 
+// (coherent: the kernel before, which may have written the logits, can still run when this one starts)
 __device__ __forceinline__ uint4 ld_once(const void* p) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;

@@ -79,7 +79,7 @@ struct I8Op {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int c = part + 2 * i, n = n0 + c * 32 + lane;
-            if (c < BN / 32) ws[i * 32 + lane] = n < p.N ? __ldg(p.w_scale + n) : 0.0f;
+            if (c < BN / 32) ws[i * 32 + lane] = n < p.N ? p.w_scale[n] : 0.0f;
         }
         __syncwarp();
         return m < p.M ? p.x_scale[m] : 0.0f;
@@ -460,7 +460,7 @@ linear_i8_rows_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_con
         if (warp >= 2 && !*s_abort && my_tiles > 0 && n < p.N) {
             const float* xs = reinterpret_cast<const float*>(smem + S::OFF_XS);
             const Seg& sg = segment_of(p, n);
-            const float4 ws = __ldg(reinterpret_cast<const float4*>(p.w_scale + n));
+            const float4 ws = *reinterpret_cast<const float4*>(p.w_scale + n);
 #pragma unroll 2
             for (int m = rank + (warp - 2) * kSplits; m < m_here; m += 4 * kSplits) {
                 int4 v[kSplits];

@@ -144,7 +144,7 @@ __device__ __forceinline__ uint32_t block_max(uint32_t m, uint32_t* slot) {
 // stay in registers; NV == 0: a longer row is read twice (the second time from L2).
 template <typename T, int WARPS, int NV>
 __global__ void __launch_bounds__(WARPS * 32)
-quantize_rows_kernel(const T* __restrict__ x, int cols, int8_t* __restrict__ q, float* __restrict__ scale) {
+quantize_rows_kernel(const T* x, int cols, int8_t* q, float* scale) {
     constexpr int NT = WARPS * 32;
     __shared__ uint32_t slot[WARPS];
     // In this order: a product launched behind this kernel may read its weights as soon as
