@@ -363,8 +363,13 @@ void gdn_norm_config_default(gdn_norm_config* cfg);
  *      y NULL (then w_pre and y_scale must be NULL): only the residual sum
  * r may be x, and y (not in int8) may be o; no other two tensors may overlap.
  * Tensors are 16-byte aligned (y_scale and a token gate: to their element).
- * T == 0 is a no-op.  A row whose sum of squares is beyond fp32 (entries above about
- * 1e19 / sqrt(dim)) has the norm 0; one with an infinity or a NaN gives NaN.
+ * T == 0 is a no-op.  The norm of a row whose sum of squares is beyond fp32 (entries
+ * above about 1e19 / sqrt(dim)) is 0.  Of a row that holds a NaN it is NaN throughout; of
+ * one that holds an infinity, as the formula has it: NaN where the infinity stands and 0
+ * in every other entry.  So an infinity in o (under w_post) makes one entry of r NaN and
+ * leaves the others x, and makes the row of y NaN; one in x, or in o without w_post,
+ * stays in r and makes one entry of y NaN and the others 0.  As 8-bit rows, every row
+ * of y with a NaN has the scale NaN and zeros.
  */
 gdn_status gdn_block_norm(const gdn_norm_config* cfg, const void* o, const void* x, const void* gate,
                           const float* w_post, const float* w_pre, int64_t T, void* r, void* y,

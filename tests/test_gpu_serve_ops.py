@@ -149,6 +149,37 @@ def test_block_norm_rows_not_finite_or_zero():
             assert torch.isnan(y[2]).all() and torch.isnan(y[1, 7])
 
 
+@pytest.mark.parametrize("T,D,dt", [(6, 2560, "bf16"), (400, 1336, "f32"), (400, 2560, "bf16")])
+def test_block_norm_of_infinities_and_overflow(T, D, dt):
+    """What gdn.h says of rows that hold an infinity or a NaN, and of finite ones beyond fp32's
+    squares, entry by entry."""
+    cfg = gdn.NormConfig(dim=D, act_dtype=DT[dt], res_dtype=DT[dt])
+    inf, nan = float("inf"), float("nan")
+    only = lambda t, row, at, rest: torch.isnan(t[row, at]) and torch.equal(
+        torch.cat([t[row, :at], t[row, at + 1:]]), torch.cat([rest[:at], rest[at + 1:]]))
+    c = norm_case(T, D, "none", dt, dt, 12)
+    x, o, zero = c["x"], c["o"], torch.zeros(D, dtype=DT[dt], device=DEV)
+    x[0, 7], o[1, 9], o[2, 11], x[3, 1], x[4] = inf, -inf, nan, nan, 1e19 * torch.sign(x[4].float()).to(DT[dt])
+    o[5, ::2] = 1e19
+    r, y, _ = gdn.block_norm(cfg, o, x, None, c["w_post"], c["w_pre"])
+    assert r[0, 7] == inf and torch.isfinite(r[0]).sum() == D - 1 and only(y, 0, 7, zero)
+    assert only(r, 1, 9, x[1]) and torch.isnan(y[1]).all()
+    assert torch.isnan(r[2]).all() and torch.isnan(y[2]).all()
+    assert torch.isnan(r[3, 1]) and torch.isfinite(r[3]).sum() == D - 1 and torch.isnan(y[3]).all()
+    assert not y[4].any() and torch.equal(r[5], x[5])          # finite, but their squares are not
+    _, q, s = gdn.block_norm(cfg, o, x, None, c["w_post"], c["w_pre"], quantize=True)
+    assert torch.isnan(s[:4]).all() and not q[:5].any() and s[4] == 0 and torch.isfinite(s[5])
+    # no norm after the block
+    r, y, _ = gdn.block_norm(cfg, o, x, None, None, c["w_pre"])
+    assert r[1, 9] == -inf and torch.isfinite(r[1]).sum() == D - 1 and only(y, 1, 9, zero)
+    assert torch.isnan(r[2, 11]) and torch.isfinite(r[2]).sum() == D - 1 and torch.isnan(y[2]).all()
+    # no block
+    _, y, _ = gdn.block_norm(cfg, None, x, None, None, c["w_pre"])
+    assert only(y, 0, 7, zero) and torch.isnan(y[3]).all() and not y[4].any() and torch.isfinite(y[1]).all()
+    _, q, s = gdn.block_norm(cfg, None, x, None, None, c["w_pre"], quantize=True)
+    assert torch.isnan(s[[0, 3]]).all() and not q[[0, 3, 4]].any() and s[4] == 0
+
+
 # ---------------------------------------------------------------------------
 # 8-bit rows and projections
 # ---------------------------------------------------------------------------
