@@ -67,7 +67,9 @@ __device__ __forceinline__ float block_sum(float v, float* slot) {
     return v;
 }
 
-// 1 / (1 + exp(-g))
+// 1 / (1 + exp(-g)).  __expf is off by 2 + 1.173 |g| ulp, the sum by half a one, __fdividef by 2
+// (and 0 for a sum above 2^126, i.e. g < -87.33): (5 + 1.2 |g|) 2^-23 of the result, below a bf16
+// rounding wherever it is not 0.
 __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
 
 // Blocks an SM shall hold: 1024 threads of them where a thread's loads in flight (2 TA, 1 TR)

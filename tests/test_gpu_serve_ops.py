@@ -149,6 +149,29 @@ def test_block_norm_rows_not_finite_or_zero():
             assert torch.isnan(y[2]).all() and torch.isnan(y[1, 7])
 
 
+@pytest.mark.parametrize("T", [8, 600])
+@pytest.mark.parametrize("gate", ["token", "channel", "full"])
+def test_block_norm_sigmoid_of_large_gates(gate, T):
+    """o = 1 and x = 0 make r the gate's factor itself: within the error that gdn.h states (from
+    the stated errors of the exponential, 2 + 1.173 |g| ulp, the sum, 1/2, and the quotient, 2)."""
+    D = 1024
+    rng = np.random.default_rng(31)
+    n = T if gate == "token" else D
+    g = np.concatenate([[-80.0, -20.0, -87.0, 20.0, 80.0, 0.0, -1e-30, -0.0], rng.uniform(-87.2, 100, max(n - 8, 0))])
+    g = g if gate != "full" else np.stack([rng.permutation(g) for _ in range(T)])
+    cfg = gdn.NormConfig(dim=D, gate=gate, gate_act="sigmoid", act_dtype=torch.float32, res_dtype=torch.float32)
+    run = lambda g: gdn.block_norm(cfg, torch.ones((T, D), device=DEV), torch.zeros((T, D), device=DEV), g)[0]
+    g = on(g)
+    ref = 1 / (1 + np.exp(-f64(g)))
+    lim = (5 + 1.2 * np.abs(f64(g))) * 2 * S.U32 * ref
+    wide = lambda a: a[:, None] + np.zeros((T, D)) if gate == "token" else a + np.zeros((T, D))
+    assert worst(np.abs(f64(run(g)) - wide(ref)), wide(lim)) <= 1
+    # beyond: 0 and 1
+    for value, want in ((-88.0, 0.0), (-1e30, 0.0), (-math.inf, 0.0), (1e30, 1.0), (math.inf, 1.0)):
+        assert torch.equal(run(torch.full_like(g, value)), torch.full((T, D), want, device=DEV))
+    assert torch.isnan(run(torch.full_like(g, math.nan))).all()
+
+
 @pytest.mark.parametrize("T,D,dt", [(6, 2560, "bf16"), (400, 1336, "f32"), (400, 2560, "bf16")])
 def test_block_norm_of_infinities_and_overflow(T, D, dt):
     """What gdn.h says of rows that hold an infinity or a NaN, and of finite ones beyond fp32's
