@@ -379,7 +379,9 @@ gdn_status gdn_block_norm(const gdn_norm_config* cfg, const void* o, const void*
 /*
  * Rows in 8-bit integers with one scale each, symmetric about zero:
  *   scale = max_k |x_k| / 127,  q_k = rint(127 x_k / max_k |x_k|)   (ties to even)
- * so x_k is about scale q_k, to half a scale.  A row of zeros has the scale 0 and
+ * so x_k is about scale q_k, to half a scale.  q is that of the formula for bf16 rows; for
+ * float32 rows 127 x_k and then the quotient are rounded to fp32 first, which can move
+ * a quotient within 2^-23 (relative) of a half to its other side.  A row of zeros has the scale 0 and
  * zeros.  A row that holds an infinity or a NaN has the scale NaN and zeros: what
  * is computed from it is NaN.  For activations a row is a token; for a weight
  * [N][K] it is an output channel.

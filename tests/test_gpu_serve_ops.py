@@ -246,6 +246,28 @@ def test_quantize_rows_f32():
     assert np.abs(f64(q) - t).max() <= 0.5 + 127 * 2 * S.U32
 
 
+@pytest.mark.parametrize("rows,cols", [(9, 2560), (400, 2560), (700, 1040), (2, 16400)])
+def test_quantize_rows_f32_is_that_of_two_fp32_operations(rows, cols):
+    """Bit for bit, at both ends of the range too, with many quotients at a half and next to one."""
+    rng = np.random.default_rng(rows + cols)
+    x = rng.normal(size=(rows, cols)).astype(np.float32)
+    x[:, 0] = rng.uniform(3.5, 7, rows)                      # the largest entry, and quotients k + 1/2 of it
+    half = (rng.integers(-127, 127, (rows, cols // 2)) + 0.5) / 127 * x[:, :1].astype(np.float64)
+    x[:, 1:1 + cols // 2] = half.astype(np.float32)
+    with np.errstate(over="ignore"):
+        x[1::3] *= np.float32(2.0 ** 120)
+        x[2::3] *= np.float32(2.0 ** -100)
+        big = np.abs(x.astype(np.float64)).max(-1, keepdims=True)
+        # (in fp64, so that 127 x stays in range; rounded to 24 bits each time, by way of [1, 2))
+        def fp32(v):
+            m, e = np.frexp(v)
+            return np.ldexp(m.astype(np.float32).astype(np.float64), e)
+        want = np.rint(fp32(fp32(127.0 * x.astype(np.float64)) / big))
+    q, s = gdn.quantize_rows(on(x))
+    np.testing.assert_array_equal(f64(q), want)
+    np.testing.assert_array_equal(s.cpu().numpy(), np.abs(x).max(-1) / np.float32(127))
+
+
 def i8_case(M, N, K, seed, x_dt="i8"):
     g = torch.Generator(device=DEV).manual_seed(seed)
     w = torch.randint(-128, 128, (N, K), generator=g, device=DEV, dtype=torch.int8)
