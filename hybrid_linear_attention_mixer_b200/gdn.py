@@ -468,6 +468,11 @@ def _shaped(t, name, dtype, index, shape):
     raise ValueError("%s must be contiguous" % name)
 
 
+def _too_large(what, *sizes):
+    """The error of a size that the library takes as 32 bits (ctypes would cut it off)."""
+    return ValueError("%s beyond 32 bits: %s" % (what, ", ".join(str(n) for n in sizes)))
+
+
 # The current stream's handle by device index: the binding's own lookup where torch has it
 # (a Stream object costs several times as much to make as the call's other arguments).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
@@ -528,6 +533,8 @@ def block_norm(cfg: NormConfig, o, x, gate=None, w_post=None, w_pre=None, r=None
     Returns (r, y, y_scale), None for what there is not."""
     dev = _index_of(x, "x")
     T, D = x.shape[0], cfg.dim
+    if D >> 31:
+        raise _too_large("dim", D)
     act, res = cfg.act_dtype, cfg.res_dtype
     px = _shaped(x, "x", res, dev, (T, D))
     po = pg = pp = pw = pr = py = ps = None
@@ -571,6 +578,8 @@ def quantize_rows(x, q=None, scale=None, stream=None):
     if x.dim() != 2:
         raise ValueError("x [rows, cols] expected, got %s" % (tuple(x.shape),))
     rows, cols = x.shape
+    if cols >> 31:
+        raise _too_large("cols", cols)
     if x.dtype not in _DT:
         raise TypeError("x: dtype %s, expected bfloat16 or float32" % x.dtype)
     px = _shaped(x, "x", x.dtype, dev, (rows, cols))
@@ -584,6 +593,8 @@ def quantize_rows(x, q=None, scale=None, stream=None):
 
 
 def linear_i8_workspace_size(M: int, K: int) -> int:
+    if K >> 31 > 0:
+        raise _too_large("K", K)
     return int(lib().gdn_linear_i8_workspace_size(int(M), int(K)))
 
 
@@ -622,6 +633,8 @@ def linear_i8(x, w, w_scale, x_scale=None, outs=None, out_dtype=torch.bfloat16, 
         raise ValueError("x [M, K] and w [N, K] expected, got %s and %s" % (tuple(x.shape), tuple(w.shape)))
     M, K = x.shape
     N = w.shape[0]
+    if (N | K) >> 31:
+        raise _too_large("N, K", N, K)
     if outs is None:
         outs = [_empty((M, N), out_dtype, dev, stream)]
     if not 1 <= len(outs) <= LINEAR_MAX_SEGMENTS:
@@ -647,6 +660,8 @@ def in_proj_i8(cfg: Config, hidden, w_in, w_scale, hidden_scale=None, out: dict 
     scales [rows of w_in]; hidden as x in ``linear_i8``."""
     dev = _index_of(hidden, "hidden")
     T, D = hidden.shape
+    if D >> 31:
+        raise _too_large("d_model", D)
     qk, vz, ab = cfg.n_k_heads * cfg.d_k, cfg.n_v_heads * cfg.d_v, cfg.n_v_heads
     N = 2 * qk + 2 * vz + 2 * ab
     widths = (("q", qk), ("k", qk), ("v", vz), ("z", vz), ("a", ab), ("b", ab))
@@ -672,6 +687,8 @@ def out_proj_i8(cfg: Config, o, w_out, w_scale, o_scale=None, y=None, workspace=
     dev = _index_of(o, "o")
     o2 = o.reshape(o.shape[0], -1) if o.is_contiguous() else o
     T, K, D = o2.shape[0], cfg.n_v_heads * cfg.d_v, w_out.shape[0]
+    if D >> 31:
+        raise _too_large("d_model", D)
     if y is None:
         y = _empty((T, D), torch.bfloat16, dev, stream)
     px, xdt, pxs, ws, ws_bytes, workspace = _i8_operand(o2, o_scale, "o", dev, T, K, workspace, stream)
@@ -682,6 +699,8 @@ def out_proj_i8(cfg: Config, o, w_out, w_scale, o_scale=None, y=None, workspace=
 
 
 def beam_workspace_size(n_groups: int, n_beams: int, vocab: int, n_out: int, logits_dtype=torch.bfloat16) -> int:
+    if (n_groups | n_beams | vocab | n_out) >> 31 > 0:
+        raise _too_large("n_groups, n_beams, vocab, n_out", n_groups, n_beams, vocab, n_out)
     return int(lib().gdn_beam_workspace_size(n_groups, n_beams, vocab, n_out, _DT[logits_dtype]))
 
 
@@ -705,6 +724,8 @@ def beam_select(logits, scores, n_out=None, finished=None, pad_token=0, parents=
     dt = _DT[logits.dtype]
     if n_out is None:
         n_out = W
+    if (G | W | V | n_out | abs(pad_token)) >> 31:
+        raise _too_large("groups, beams, vocab, n_out, pad_token", G, W, V, n_out, pad_token)
     ld = V
     if not logits.is_contiguous():
         ld = logits.stride(1) if W > 1 else logits.stride(0) if G > 1 else V
@@ -738,6 +759,8 @@ class ReorderPlan:
         # caller points a tensor at other memory)
         self.states = [t.detach() for t in states]
         self.n_groups, self.n_beams = int(n_groups), int(n_beams)
+        if (self.n_groups | self.n_beams) >> 31:
+            raise _too_large("n_groups, n_beams", n_groups, n_beams)
         self.device = _index_of(states[0], "states[0]")
         self.buffers = (_CStateBuffer * len(states))()
         for i, t in enumerate(self.states):

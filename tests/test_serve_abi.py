@@ -265,6 +265,36 @@ def test_reorder_plan_keeps_its_memory(monkeypatch):
     assert all(int(torch.count_nonzero(t)) == 0 for t in plan.states)
 
 
+def test_binding_refuses_sizes_that_the_library_cannot_take(monkeypatch):
+    """Sizes that are 32 bits in the C interface are not cut off to other sizes (shapes alone
+    here: tensors without memory, and no call may get as far as the library)."""
+    monkeypatch.setattr(gdn, "_index_of", lambda t, name: t.get_device())
+    reached = lambda *a: pytest.fail("reached the library")
+    monkeypatch.setattr(gdn, "_call", reached)
+    over = 2 ** 32
+    e = lambda *s, dt=torch.bfloat16: torch.empty(s, dtype=dt, device="meta")
+    f, i8 = (lambda *s: e(*s, dt=torch.float32)), (lambda *s: e(*s, dt=torch.int8))
+    lg, sc = f(2, 3, 1000), f(2, 3)
+    layer = gdn.Config()
+    for bad in (lambda: gdn.block_norm(gdn.NormConfig(dim=over + 64), None, e(1, over + 64), w_pre=f(over + 64)),
+                lambda: gdn.quantize_rows(e(1, over + 64)),
+                lambda: gdn.linear_i8(i8(1, over + 64), i8(8, over + 64), f(8), x_scale=f(1)),
+                lambda: gdn.linear_i8(i8(1, 64), i8(over + 8, 64), f(over + 8), x_scale=f(1)),
+                lambda: gdn.in_proj_i8(layer, i8(1, over + 64), i8(16480, over + 64), f(16480), hidden_scale=f(1)),
+                lambda: gdn.out_proj_i8(layer, i8(1, 6144), i8(over + 64, 6144), f(over + 64), o_scale=f(1)),
+                lambda: gdn.beam_select(lg, sc, pad_token=over),
+                lambda: gdn.beam_select(lg, sc, pad_token=-over),
+                lambda: gdn.beam_select(lg, sc, n_out=over + 3),
+                lambda: gdn.beam_select(lg, sc, n_out=-1),
+                lambda: gdn.beam_select(f(over, 1, 1), f(over, 1)),
+                lambda: gdn.reorder_states(e(over, 1, dt=torch.int32), [f(over, 4)]),
+                lambda: gdn.linear_i8_workspace_size(4, over + 64),
+                lambda: gdn.beam_workspace_size(2, 3, 1000, over + 4),
+                lambda: gdn.beam_workspace_size(2, over + 3, 1000, 4)):
+        with pytest.raises(ValueError):
+            bad()
+
+
 def test_status_string_of_the_index_check():
     assert gdn.status_string(8) not in {gdn.status_string(s) for s in range(8)} | {"unknown status"}
 
