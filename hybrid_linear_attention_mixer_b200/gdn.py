@@ -378,7 +378,7 @@ def out_proj(cfg: Config, o, w_out, y=None, stream=None):
     """The mixer's output projection: o [T, H_v*d_v] bf16 (the layer's output),
     w_out [d_model, H_v*d_v] bf16 -> y [T, d_model] bf16."""
     dev = o.device
-    o2 = o.reshape(o.shape[0], -1)
+    o2 = o.flatten(1) if o.dim() > 1 else o.reshape(-1, 1)
     T = o2.shape[0]
     D = w_out.shape[0]
     _check(o2, "o", torch.bfloat16, dev)
@@ -685,7 +685,7 @@ def out_proj_i8(cfg: Config, o, w_out, w_scale, o_scale=None, y=None, workspace=
     """The mixer's output projection in 8-bit integers: ``out_proj`` with w_out int8 and its
     scales [d_model]; o as x in ``linear_i8``.  y [T, d_model] bf16."""
     dev = _index_of(o, "o")
-    o2 = o.reshape(o.shape[0], -1) if o.is_contiguous() else o
+    o2 = o.flatten(1) if o.dim() > 2 and o.is_contiguous() else o
     T, K, D = o2.shape[0], cfg.n_v_heads * cfg.d_v, w_out.shape[0]
     if D >> 31:
         raise _too_large("d_model", D)

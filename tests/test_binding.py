@@ -55,6 +55,24 @@ def test_projection_shapes():
         gdn.out_proj(cfg, bf16(4, 6144), bf16(2560, 4096), stream=NULL_STREAM)
 
 
+def test_output_projections_of_no_tokens(monkeypatch):
+    """A batch without tokens is nothing to do, in the mixer's own layout (heads apart) too."""
+    cfg, w = gdn.Config(), bf16(2560, 6144)
+    monkeypatch.setattr(gdn, "_index_of", lambda t, name: t.get_device())
+    monkeypatch.setattr(gdn, "_call", lambda fn, what, index, stream, *a: fn(*a, None) and pytest.fail(what))
+    monkeypatch.setattr(gdn, "_empty", lambda shape, dtype, index, stream: torch.empty(shape, dtype=dtype))
+    w8, ws = torch.zeros((2560, 6144), dtype=torch.int8), torch.ones(2560)
+    for shape in ((0, 6144), (0, 48, 128)):
+        assert gdn.out_proj(cfg, bf16(*shape), w, stream=NULL_STREAM).shape == (0, 2560)
+        assert gdn.out_proj_i8(cfg, bf16(*shape), w8, ws).shape == (0, 2560)
+        assert gdn.out_proj_i8(cfg, bf16(*shape).to(torch.int8), w8, ws, o_scale=torch.ones(0)).shape == (0, 2560)
+    for o in (bf16(0), bf16(4), bf16(0, 48), bf16(4, 6144).t()):
+        with pytest.raises(ValueError):
+            gdn.out_proj(cfg, o, w, stream=NULL_STREAM)
+        with pytest.raises(ValueError):
+            gdn.out_proj_i8(cfg, o, w8, ws)
+
+
 def test_decode_multi_rows_must_split_into_tokens():
     cfg = gdn.Config()
     q = bf16(6, 16, 128)
