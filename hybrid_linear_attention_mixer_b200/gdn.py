@@ -804,7 +804,12 @@ def check_device_error(stream=None) -> None:
     """Synchronise the stream and raise GdnError if the device error word holds an
     error: a bounded wait that ran out, a failed device check of a prefill's
     inputs (malformed cu_seqlens, conv output beyond fp16), or a parent outside its
-    group in reorder_states."""
+    group in reorder_states.  Every device has its own word: the one read is that of the
+    stream's device (without a stream: of the current one)."""
+    index = getattr(stream, "device_index", None)
+    if index is not None and index != _current_device():
+        with torch.cuda.device(index):
+            return check_device_error(stream)
     s = lib().gdn_check_device_error(_stream(stream))
     if s != 0:
         raise GdnError(s, "device")

@@ -73,6 +73,33 @@ def test_output_projections_of_no_tokens(monkeypatch):
             gdn.out_proj_i8(cfg, o, w8, ws)
 
 
+def test_device_errors_are_those_of_the_streams_device(monkeypatch):
+    """A call on another device than the current one leaves its error there."""
+    now, words = [0], {0: 0, 1: 8}
+
+    class device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.before, now[0] = now[0], self.index
+
+        def __exit__(self, *a):
+            now[0] = self.before
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(gdn, "_current_device", lambda: now[0])
+    real = gdn.lib()
+    monkeypatch.setattr(gdn, "lib", lambda: types.SimpleNamespace(gdn_check_device_error=lambda s: words[now[0]],
+                                                                  gdn_status_string=real.gdn_status_string))
+    stream = lambda index: types.SimpleNamespace(cuda_stream=0, device_index=index)
+    gdn.check_device_error(stream(0))
+    gdn.check_device_error(NULL_STREAM)
+    with pytest.raises(gdn.GdnError) as e:
+        gdn.check_device_error(stream(1))
+    assert e.value.status == 8 and now == [0]
+
+
 def test_decode_multi_rows_must_split_into_tokens():
     cfg = gdn.Config()
     q = bf16(6, 16, 128)
