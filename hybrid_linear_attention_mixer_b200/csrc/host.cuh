@@ -24,9 +24,11 @@ inline bool dim_ok(int d) { return d == 32 || d == 64 || d == 128; }
 inline thread_local cudaError_t t_last_cuda_error = cudaSuccess;
 
 // GDN_OK for cudaSuccess; otherwise remembers e for this thread and returns GDN_ERR_CUDA.
+// (The runtime's own last error is taken, or the next launch would be said to have failed.)
 inline gdn_status cuda_status(cudaError_t e) {
     if (e == cudaSuccess) return GDN_OK;
     t_last_cuda_error = e;
+    (void)cudaGetLastError();
     return GDN_ERR_CUDA;
 }
 

@@ -155,3 +155,22 @@ def test_products_behind_a_kernel_that_lets_them_start_and_runs_on(M, N, K, x_dt
     gdn.linear_i8(x, w, ws, outs=[out], workspace=work, **kw)
     gdn.check_device_error()
     assert torch.equal(out, ref)
+
+
+def test_a_calls_cuda_error_is_its_own():
+    """A CUDA call that fails inside one of the library's calls (here: a synchronisation while
+    the stream is captured, which ends that capture) is that call's error, and not the next's."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    x, w = (torch.randn(s, generator=g, device=DEV).to(torch.bfloat16) for s in ((40, 256), (264, 256)))
+    ref = gdn.linear(x, w)[0]
+    torch.cuda.synchronize()
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.stream(stream):
+        graph.capture_begin()
+        with pytest.raises(gdn.GdnError) as e:
+            gdn.check_device_error(stream)
+        with pytest.raises(RuntimeError):
+            graph.capture_end()
+    assert e.value.status == gdn.CUDA_ERROR
+    assert torch.equal(gdn.linear(x, w)[0], ref)
+    gdn.check_device_error()
