@@ -128,6 +128,35 @@ def test_block_norm_to_i8(T, D):
     assert np.abs(f64(q)).max(-1).min() == 127
 
 
+# Both sides of every bound between the forms for many rows (more than two to an SM), by dim.
+MANY_DIMS = [8, 64, 504, 512, 520, 1024, 1032, 1536, 1544, 2048, 2056, 2560, 4040, 4096, 4104, 8192, 8200]
+
+
+@pytest.mark.parametrize("D", MANY_DIMS)
+@pytest.mark.parametrize("act,res", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16"), ("f32", "f32")])
+def test_block_norm_many_rows(D, act, res):
+    """The forms for many rows against the reference, in every type, to 8 bits too."""
+    T = 2 * torch.cuda.get_device_properties(0).multi_processor_count + 5
+    gate = ("none", "token", "channel", "full")[(D // 8 + len(act + res)) % 4]
+    cfg = gdn.NormConfig(dim=D, res_scale=0.75, gate=gate, gate_act="sigmoid", act_dtype=DT[act], res_dtype=DT[res])
+    c = norm_case(T, D, gate, act, res, D)
+    args = (cfg, c["o"], c["x"], c["gate"], c["w_post"], c["w_pre"])
+    r, y, _ = gdn.block_norm(*args)
+    check_norm(c, cfg, r, y, act, res)
+    r8, q, scale = gdn.block_norm(*args, quantize=True)
+    assert torch.equal(r8, r)
+    rr, ry, p = norm_ref(c, cfg)
+    _, ey = S.block_norm_bounds(rr, ry, p)
+    sc, ref = f64(scale), np.abs(ry).max(-1) / 127           # the bounds of test_block_norm_to_i8
+    assert worst(np.abs(sc - ref), ey.max(-1) / 127 + 2 * S.U32 * ref) <= 1
+    assert worst(np.abs(f64(q) * sc[:, None] - ry), 0.5 * sc[:, None] + ey + 4 * S.U32 * np.abs(ry)) <= 1
+    assert np.abs(f64(q)).max(-1).min() == 127
+    # the commonest call: a residual sum and the norm before the next block, nothing else
+    plain = gdn.NormConfig(dim=D, act_dtype=DT[act], res_dtype=DT[res])
+    r, y, _ = gdn.block_norm(plain, c["o"], c["x"], None, None, c["w_pre"])
+    check_norm(dict(c, gate=None, w_post=None), plain, r, y, act, res)
+
+
 def test_block_norm_rows_not_finite_or_zero():
     """Infinities and NaN stay in their rows; a row of zeros has the norm zero."""
     T, D = 6, 2560
@@ -215,6 +244,34 @@ def test_quantize_rows_bf16_is_exact(rows, cols):
     rq, rs = S.quantize_rows(f64(x))
     np.testing.assert_array_equal(f64(q), rq)
     np.testing.assert_array_equal(s.cpu().numpy(), (f64(x.abs().amax(-1)).astype(np.float32) / np.float32(127)))
+
+
+@pytest.mark.parametrize("cols", [16, 512, 1024, 1040, 2560, 2576, 6144, 6160, 8192, 8208])
+def test_quantize_rows_many_rows(cols):
+    """Both sides of every bound between the forms, by columns, for more rows than two to an SM:
+    exact in bf16, and half a step (and two roundings) in fp32."""
+    rows = 2 * torch.cuda.get_device_properties(0).multi_processor_count + 7
+    rng = np.random.default_rng(cols)
+    x = on(rng.normal(size=(rows, cols)) * np.exp(rng.normal(size=(rows, 1)) * 20), "bf16")
+    q, s = gdn.quantize_rows(x)
+    rq, _ = S.quantize_rows(f64(x))
+    np.testing.assert_array_equal(f64(q), rq)
+    np.testing.assert_array_equal(s.cpu().numpy(), x.float().abs().amax(-1).cpu().numpy() / np.float32(127))
+    x = on(rng.normal(size=(rows, cols)))
+    q, s = gdn.quantize_rows(x)
+    t = 127 * f64(x) / np.abs(f64(x)).max(-1, keepdims=True)
+    assert np.abs(f64(q) - t).max() <= 0.5 + 127 * 2 * S.U32
+    np.testing.assert_array_equal(s.cpu().numpy(), x.abs().amax(-1).cpu().numpy() / np.float32(127))
+
+
+@pytest.mark.parametrize("M,N,K", [(400, 264, 2560), (330, 1000, 1040), (600, 136, 6144), (301, 2312, 512)])
+@pytest.mark.parametrize("x_dt", ["bf16", "f32"])
+def test_linear_i8_makes_many_rows(M, N, K, x_dt):
+    x, _, w, ws = i8_case(M, N, K, M + N + K, x_dt)
+    y = gdn.linear_i8(x, w, ws, out_dtype=torch.float32)[0]
+    q, xs = gdn.quantize_rows(x)
+    assert torch.equal(y, gdn.linear_i8(q, w, ws, x_scale=xs, out_dtype=torch.float32)[0])
+    check_linear(y, x, None, w, ws, "f32")
 
 
 def test_quantize_rows_bf16_ties_and_range():
