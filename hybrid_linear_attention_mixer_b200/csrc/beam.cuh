@@ -14,8 +14,9 @@
 // these maxima (or of maxima over several tiles) reach is reached by at least n logits; a
 // few bisection steps find one that not many more reach.  The vectors behind the tile
 // maxima that reach it are read once more (from L2), and the logits that do are ranked
-// exactly, by 64-bit keys (logit, then lowest index).  Where ties make them too many (a row of equal logits), the
-// bound is found exactly, over logits and then over indexes, by more such readings.
+// exactly, by 64-bit keys (logit, then lowest index).  Where ties make them too many (a row of
+// equal logits), the bound is found exactly, over logits and then over indexes, by more such
+// readings.
 // Nothing synchronises warps, so one's selection runs beside the others' streams.
 //
 // 64 requests of 8 beams x 248,320 bf16 logits, 16 results: 63 us (4.0 TB/s), 57 of it the
@@ -253,8 +254,8 @@ __device__ __forceinline__ float find_bound(const float (&mine)[GROUPS], float t
 }
 
 // The fast sum: exp(x) / 2^c is 2^(x log2e - c) in one fused operation, c an integer near
-// the largest x so far.  log2e in fp32 is 1.3e-8 (kScale) too large, which scales x: that
-// is taken back at the slice's top, so what is left goes by the distance from it.
+// the largest x so far.  log2e in fp32 is off by 1.3e-8 of itself (too small: kScale < 0), which
+// scales x: that is taken back at the slice's top, so what is left goes by the distance from it.
 // kSpan: how far above c a maximum may lie; kMaxTop: the size of x up to which c is exact.
 constexpr float kSpan = 32.0f, kMaxTop = 65536.0f;
 constexpr double kScale = (double)kLog2e * kLn2 - 1.0;

@@ -116,8 +116,13 @@ cudaError_t launch_quantize(const void* x, int64_t rows, int32_t cols, int8_t* q
     const T* xt = static_cast<const T*>(x);
     const unsigned grid = (unsigned)rows;
     const int nv = cols / 8;
-    // Few rows: a vector per thread, the lowest latency.  Many: few warps with several
-    // vectors each (32,768 rows of 2560: 47 us with 2 warps, 55 with 5, 72 with 10).
+    // Few rows: a vector per thread, the lowest latency.  Many: the fewest warps that hold the
+    // row, with several vectors each.  168 M elements in bf16, us (floor 78; blocks of 2 warps
+    // and 5 vectors / 4 and 6 / 8 and 4): 1040 columns 170 / 211 / 293, 1536 116 / 152 / 207,
+    // 2560 79 / 113 / 150, then - / 115 / 152 at 2576, 4096 - / 90 / 112, 6144 - / 80 / 94; from
+    // fp32 (floor 130) 170 / 281 / 385 at 1040, 125 / 151 / 197 at 2560, - / 123 / 125 at 6144.
+    // Up to 1024 columns every form takes 1.05 ns a row, the rate at which blocks start (1024:
+    // 172 us, 512: 340), and the last one any length.
     if (nv <= 128) return Launch(grid, 128, 0, st)(quantize_rows_kernel<T, 4, 1>, xt, cols, q, scale);
     if (nv <= 320 && rows <= 2 * sm_count()) return Launch(grid, 320, 0, st)(quantize_rows_kernel<T, 10, 1>, xt, cols, q, scale);
     if (nv <= 320) return Launch(grid, 64, 0, st)(quantize_rows_kernel<T, 2, 5>, xt, cols, q, scale);
@@ -190,8 +195,7 @@ cudaError_t launch_i8_pair(const void* x, const void* w, gdn::gemm::I8Args a, cu
 
 // Pair tile width for M > 128, over the widths that kind::i8 has at M = 256: fewest
 // waves x (operand bytes of a k-block, 128 x (256 + BN) of a pair).  The bytes from L2 bound
-// a k-block, not the MMA, which takes half the bf16 form's time: 4096 x 16480 x 2560 at 256
-// (15 waves) 127 us, at 224 (16) 131, at 192 (19) 142; the bf16 form's rule took 224.
+// a k-block, not the MMA: 4096 x 16480 x 2560 at 256 (15 waves) 127 us, at 224 (16) 131, at 192 (19) 142; the bf16 form's rule took 224.
 // *cost: those bytes of one CTA in units of 128 times K's k-blocks, as for the other form.
 int pick_bn_i8(int64_t M, int N, int pairs, int64_t* cost_out) {
     static const int cand[] = {256, 224, 192, 160, 128};
@@ -211,7 +215,7 @@ int pick_bn_i8(int64_t M, int N, int pairs, int64_t* cost_out) {
 }
 
 constexpr int kMinTileRows = 96, kJoinCost = 250, kBlocksCost = 950;
-constexpr int64_t kMaxRowsM = 148 * 128;   // no more blocks of tokens than SMs
+constexpr int64_t kMaxRowsM = 148 * 128;   // more blocks of tokens than SMs need no plan
 
 template <int BT, int kSplits, int XQ>
 struct RowsForm {
@@ -399,7 +403,9 @@ gdn_status run_linear_i8(const void* x, int32_t x_dtype, const float* x_scale, c
 // Beam selection
 // ---------------------------------------------------------------------------
 constexpr int kBeamTiles = 2;
-constexpr int kBeamWarps = 148 * 32;    // the slice warps that the GPU holds
+// The slice warps that a B200 holds: fixed, not asked of the device, since the workspace's
+// size follows from it and may be asked for where there is none.
+constexpr int kBeamWarps = 148 * 32;
 
 struct BeamLayout {
     int slices, tiles;

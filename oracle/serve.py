@@ -74,11 +74,20 @@ def log_softmax(x):
         return x - m - np.log(np.exp(x - m).sum(-1, keepdims=True))
 
 
-# A thread adds exponentials in fp32 in sums of 16 at most (15 U32), each off by 2 ulp and
-# an argument rounded once or twice (below 10 U32 where it matters); log2(e) in fp32 is
-# 1.4e-8 off and scales a logit's distance from the top, below 64 where it matters; the
-# rest is in fp64.  25 U32 + 64 * 1.4e-8 < 2.5e-6 of the sum, so of the log-sum-exp
-# absolutely; twice that is allowed.  The published scores are rounded to fp32 besides.
+# What a sum of exponentials is off by, relative to itself, and so the log-sum-exp absolutely:
+# * 2^y by ex2.approx: 2^-22 = 4 U32.
+# * Its argument y = x log2(e) - c, one fused operation: the terms that matter have |y| < 32 (the
+#   largest of a lane's lies between -1 and 32, kSpan, above its c), so half a step is
+#   2^-20, times ln 2: 11.1 U32.  About the top itself (large logits) it is (x - top) log2(e),
+#   two roundings of 2 U32 d nats together at the distance d; 2^20 logits at one distance
+#   have the share 2^20 e^-d / (1 + 2^20 e^-d) of the sum, and d times that is at most 10.5:
+#   21 U32.
+# * log2(e) in fp32, off by 1.34e-8, scales those distances: 10.5 * 1.34e-8 = 2.4 U32.
+# * fp32 additions before a sum goes to fp64: chains of 8 (bf16; 4 in fp32) in four sums, joined in
+#   two more: 7 + 2 = 9 U32; about the top itself 7.
+# 4 + 11.1 + 2.4 + 9 = 27 U32 = 1.6e-6, and 4 + 21 + 2.4 + 7 = 35 U32 = 2.1e-6 about the top itself;
+# the rest is in fp64.  Below 2.5e-6; twice that is allowed.  The published scores are rounded to
+# fp32 besides.
 BEAM_ERR = 5e-6
 
 
