@@ -195,7 +195,8 @@ cudaError_t launch_i8_pair(const void* x, const void* w, gdn::gemm::I8Args a, cu
 
 // Pair tile width for M > 128, over the widths that kind::i8 has at M = 256: fewest
 // waves x (operand bytes of a k-block, 128 x (256 + BN) of a pair).  The bytes from L2 bound
-// a k-block, not the MMA: 4096 x 16480 x 2560 at 256 (15 waves) 127 us, at 224 (16) 131, at 192 (19) 142; the bf16 form's rule took 224.
+// a k-block, not the MMA: 4096 x 16480 x 2560 at 256 (15 waves) 127 us, at 224 (16) 131, at 192
+// (19) 142; the bf16 form's rule took 224.
 // *cost: those bytes of one CTA in units of 128 times K's k-blocks, as for the other form.
 int pick_bn_i8(int64_t M, int N, int pairs, int64_t* cost_out) {
     static const int cand[] = {256, 224, 192, 160, 128};
