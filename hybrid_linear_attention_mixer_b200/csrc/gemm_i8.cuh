@@ -6,7 +6,7 @@
 // Two forms:
 //   - M > 128 (prefill): the CTA-pair kernel of gemm.cuh with 128 bytes of K per
 //     k-block = 128 int8, i.e. twice the K of the bf16 form for the same operand
-//     bytes and MMA time.  Bound by those bytes from L2 (MMA pipe 75% busy at
+//     bytes and MMA time.  Bound by those bytes from L2 (MMA pipe 83% busy at
 //     4096 x 16480 x 2560), in long runs by the power cap.
 //   - M <= 128 (decode), and more tokens where few outputs leave that form's pairs idle
 //     and all tiles run at once: linear_i8_rows_kernel below, bound by reading the weights.

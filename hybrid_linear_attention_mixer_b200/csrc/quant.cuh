@@ -10,7 +10,7 @@
 // within 2^-22 of the quotient, so only a value that close to a half needs the division.
 //
 // Bound by memory, 2 (or 4) bytes read and 1 written per element: 32,768 rows of 2560 in 47 us
-// (5.4 TB/s), 4096 in 7.7; one row by latency, 1.4 us.  A row belongs to one block and stays
+// (5.4 TB/s), 4096 in 8 to 9; one row by latency, 1.6 us.  A row belongs to one block and stays
 // in its registers as loaded between the maximum and the rounding.
 #pragma once
 
