@@ -521,10 +521,14 @@ static_assert(GDN_BEAM_MAX_VOCAB <= 1 << kTokenBits && kMaxBeams <= 1 << (32 - k
 struct Cand {
     uint64_t score;   // ordered; 0: none
     uint32_t at;      // w * 2^20 + v: in the order of w * V + v
-    uint32_t rough;   // the score rounded down to fp32, ordered; 0: none
+    uint32_t logit;   // ordered
+    // the score's upper half, in the same order; 0: none
+    __device__ __forceinline__ uint32_t rough() const { return (uint32_t)(score >> 32); }
 };
+// Within a beam the logits decide: beside a score of 1e17, say, fp64 does not tell them apart.
 __device__ __forceinline__ bool better(const Cand& a, const Cand& b) {
-    return a.score > b.score || (a.score == b.score && a.at < b.at);
+    if (a.score != b.score) return a.score > b.score;
+    return a.at >> kTokenBits == b.at >> kTokenBits && a.logit != b.logit ? a.logit > b.logit : a.at < b.at;
 }
 
 // How many of c[0 .. total) are better than c[i], for the items i that the block's
@@ -561,7 +565,7 @@ __device__ __noinline__ uint32_t block_bound(const Cand* c, int total, int n, Sc
     uint32_t least = ~0u, most = 0;
     int valid = 0;
     for (int i = tid; i < total; i += MT) {
-        const uint32_t r = c[i].rough;
+        const uint32_t r = c[i].rough();
         if (r) {
             ++valid;
             least = min(least, r);
@@ -583,7 +587,7 @@ __device__ __noinline__ uint32_t block_bound(const Cand* c, int total, int n, Sc
     while (reach > n + 8 && hi > lo) {
         const uint32_t mid = lo + (hi - lo + 1) / 2;
         int k = 0;
-        for (int i = 0; i < total; i += MT) k += __syncthreads_count(i + tid < total && c[i + tid].rough >= mid);
+        for (int i = 0; i < total; i += MT) k += __syncthreads_count(i + tid < total && c[i + tid].rough() >= mid);
         if (k >= n) {
             lo = mid;
             reach = k;
@@ -702,13 +706,13 @@ __global__ void __launch_bounds__(MT) merge_kernel(const __grid_constant__ Args 
         if (kind[w] == 1) {
             const uint64_t k = keys[l * p.n + e];
             if (!k) return c;
-            score += (double)from_ordered((uint32_t)(k >> 32)) - ref[w];
+            c.logit = (uint32_t)(k >> 32);
+            score += (double)from_ordered(c.logit) - ref[w];
             c.at = (uint32_t)w << kTokenBits | (0xffffffffu - (uint32_t)k);
         } else if (kind[w] == 0 || l != w * p.slices || e != 0) {
             return c;
         }
         c.score = ordered64(score);
-        c.rough = ordered(__double2float_rd(score));
         return c;
     };
     // What n heads reach, the n best candidates reach: they are collected, and narrowed down
@@ -721,7 +725,7 @@ __global__ void __launch_bounds__(MT) merge_kernel(const __grid_constant__ Args 
         if (k < merge_cap(p.n)) cand[k] = c;
     };
     for (int l = tid; l < lists; l += MT)
-        if (head[l].rough >= bound) {
+        if (head[l].rough() >= bound) {
             collect(head[l]);
             s_list[atomicAdd(&s_lists, 1)] = (uint16_t)l;
         }
@@ -731,7 +735,7 @@ __global__ void __launch_bounds__(MT) merge_kernel(const __grid_constant__ Args 
         const int l = s_list[i >> bits], e = i & ((1 << bits) - 1);
         if (e == 0 || e >= p.n) continue;
         const Cand c = entry(l, head[l].at >> kTokenBits, e);
-        if (c.rough >= bound) collect(c);
+        if (c.rough() >= bound) collect(c);
     }
     __syncthreads();
     if (s_n > merge_cap(p.n)) {
@@ -756,7 +760,7 @@ __global__ void __launch_bounds__(MT) merge_kernel(const __grid_constant__ Args 
     if (total > kFew) {
         const uint32_t closer = block_bound(cand, total, p.n, &scratch[1]);
         for (int i = tid; i < total; i += MT)
-            if (cand[i].rough >= closer) {
+            if (cand[i].rough() >= closer) {
                 const int k = atomicAdd(&s_few, 1);
                 if (k < kFew) few[k] = cand[i];
             }

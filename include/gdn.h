@@ -439,7 +439,8 @@ gdn_status gdn_out_proj_i8(const gdn_config* cfg, const void* o, int32_t x_dtype
  * w * vocab + v comes first.  A candidate whose score is not finite is none: a
  * masked token (logit -inf), a beam not in use (score -inf), a beam whose logits
  * are all -inf or hold a NaN or a +inf.  Scores are compared in fp64 before they
- * are rounded; the sums of exponentials leave them within 5e-6 of the formula (equal
+ * are rounded, two tokens of one beam by their logits (which a large score of the beam
+ * would hide); the sums of exponentials leave them within 5e-6 of the formula (equal
  * rows of logits alike, wherever they lie).
  *   logits [n_groups*n_beams] rows of vocab entries, GDN_BF16 or GDN_F32, `ld`
  *          entries apart (ld >= vocab), aligned to an entry

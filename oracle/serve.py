@@ -108,7 +108,7 @@ def beam_select(logits, scores, n, finished=None, pad=0):
         k = min(n + 1, flat.size)
         cut = np.partition(flat, flat.size - k)[flat.size - k]
         at = np.nonzero((flat >= cut) & (flat > -np.inf))[0]
-        at = at[np.lexsort((at, -flat[at]))]
+        at = at[np.lexsort((at, -logits[g].reshape(-1)[at], at // V, -flat[at]))]   # (a beam's own by their logits)
         for a, b in zip(at[:n], at[1:n + 1]):
             if a // V != b // V and flat[a] != flat[b]:
                 gap = min(gap, flat[a] - flat[b])

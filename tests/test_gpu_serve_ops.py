@@ -559,6 +559,37 @@ def test_beam_select_masks_of_the_lowest_value(dt):
     check_beam(logits, scores, n, gdn.beam_select(logits, scores, n_out=n))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [700, 50001])
+def test_beam_select_scores_that_hide_the_logits(dt, V):
+    """Beams put out of use by a large finite score (the type's lowest value among them): fp64 does
+    not tell their tokens' scores apart, their logits do, equal ones by the lowest token."""
+    W, n = 4, 24
+    logits, _ = beam_case(6, W, V, dt, 23)
+    rng = np.random.default_rng(24)
+    keep = torch.from_numpy(rng.permutation(V)[:5]).to(DEV)
+    first = torch.full((V,), -math.inf, dtype=DT[dt], device=DEV)
+    first[keep] = torch.arange(5, device=DEV).to(DT[dt])
+    logits[:, 0] = first                                    # five tokens left in the beam in use
+    logits[5, 1] = torch.round(logits[5, 1].float()).to(DT[dt])
+    scores = torch.zeros((6, W), device=DEV)
+    for g, low in enumerate((-1e12, -1e17, -1e30, torch.finfo(torch.float32).min, -3e20, -1e30)):
+        scores[g, 1:] = low
+        scores[g, 2] = -math.inf
+    scores[4, 3] = -2e20                                    # (before beam 1)
+    p, t, s = gdn.beam_select(logits, scores, n_out=n)
+    assert not p[:, :5].any() and torch.equal(t[:, :5].long(), keep.flip(0).expand(6, 5))
+    for g in range(6):
+        if g > 0:   # (beside 1e12, with steps of 1e-4, the beams still take turns)
+            w = 3 if g == 4 else 1
+            assert (p[g, 5:] == w).all() and (s[g, 5:] == scores[g, w]).all()
+        for w in (1, 3):
+            x = logits[g, w].cpu().float().numpy().astype(np.float64)
+            mine = t[g, 5:][p[g, 5:] == w].tolist()
+            assert mine == np.lexsort((np.arange(V), -x))[:len(mine)].tolist()
+        assert ((p[g, 5:] == 1) | (p[g, 5:] == 3)).all()
+
+
 def test_beam_select_large_logits():
     """Rows with a large common offset, and of either sign of a large value."""
     G, W, V, n = 4, 2, 9000, 6
